@@ -442,6 +442,280 @@ sol_status sol_gemm_gelu(const void *A, const void *B, const void *bias,
 /* Workspace bytes sol_gemm_gelu needs for this problem on the current device. */
 size_t sol_gemm_gelu_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
+/*
+ * Training operators of the per-token path
+ * ----------------------------------------
+ * The backward passes and what a training step of the block needs next to the
+ * operations above: the layer norm, rotary positions at explicit position
+ * ids, dropout.  The conventions above hold (token rows, modulation vectors,
+ * element type, alignment, errors), and:
+ *
+ * Gradients of vectors (dgamma, dbeta, dscale, dshift, dgate) are sums over
+ * many rows.  They are fp32 arrays whatever the call's element type, 16-byte
+ * aligned, overwritten (not added to), and the same bit for bit on every
+ * call: no atomics, the order of the sums depends on the sizes only.
+ *
+ * A workspace is device scratch owned by the caller, 16-byte aligned, of at
+ * least the bytes that the call's _workspace_bytes function gives; its
+ * contents on entry do not matter.  Calls that share one must be ordered on
+ * one stream.  Such a call enqueues two kernels.
+ *
+ * A backward call with zero rows writes zeros to the gradients of vectors.
+ */
+
+/*
+ * Layer norm, with optional weight and bias and optional adaptive modulation.
+ * For every row of sample b with modality m:
+ *
+ *   n[c] = (x[c] - mean) * rstd * gamma[c] + beta[c],
+ *   rstd = 1 / sqrt(mean_c((x - mean)^2) + eps)
+ *   y[c] = n[c] * (1 + scale[b][m][c]) + shift[b][m][c]
+ *
+ *   x, y          [B, L, D] device, contiguous.  y may equal x (in place).
+ *   mean, rstd    [B, L] fp32 device, 4-byte aligned, or both NULL: the row
+ *                 statistics that sol_layer_norm_backward takes.
+ *   gamma, beta   [D] device; each may be NULL (1 and 0).
+ *   scale, shift  [B, 2, D] device, or both NULL (y = n).
+ *   n_video, D, eps  as for sol_rms_adaln (same D limit); n_video is checked
+ *                 but has no effect without scale.
+ */
+sol_status sol_layer_norm(const void *x, void *y, float *mean, float *rstd,
+                          const void *gamma, const void *beta,
+                          const void *scale, const void *shift, int64_t B,
+                          int64_t L, int64_t n_video, int64_t D, float eps,
+                          sol_dtype dtype, sol_stream_t stream);
+
+/*
+ * Gradient of sol_layer_norm.  With x^ = (x - mean) * rstd, n = x^ * gamma +
+ * beta and g = dy * (1 + scale) * gamma:
+ *
+ *   dx     = rstd * (g - mean_c(g) - x^ * mean_c(g * x^)) + dres
+ *   dgamma = sum over all rows of dy * (1 + scale) * x^
+ *   dbeta  = sum over all rows of dy * (1 + scale)
+ *   dscale[b][m] = sum over the rows of (b, m) of dy * n
+ *   dshift[b][m] = sum over the rows of (b, m) of dy
+ *
+ *   dy, x         [B, L, D] device, contiguous.
+ *   mean, rstd    [B, L] fp32, from the forward call.
+ *   gamma, beta, scale  as given to the forward call (beta matters for dscale
+ *                 only).
+ *   dres          [B, L, D] or NULL: a gradient to add, that of the residual
+ *                 stream next to the norm.
+ *   dx            [B, L, D]; may equal dy, x or dres (in place).
+ *   dgamma, dbeta [D] fp32; each may be NULL (not wanted).
+ *   dscale, dshift [B, 2, D] fp32; each may be NULL; must be NULL without
+ *                 scale.
+ *   workspace     sol_norm_backward_workspace_bytes; may be NULL when no
+ *                 gradient of a vector is wanted.
+ *   With scale, B <= 32767.  n_video, D as for sol_rms_adaln.
+ */
+sol_status sol_layer_norm_backward(
+    const void *dy, const void *x, const float *mean, const float *rstd,
+    const void *gamma, const void *beta, const void *scale, const void *dres,
+    void *dx, float *dgamma, float *dbeta, float *dscale, float *dshift,
+    int64_t B, int64_t L, int64_t n_video, int64_t D, void *workspace,
+    size_t workspace_bytes, sol_dtype dtype, sol_stream_t stream);
+
+/*
+ * Gradient of sol_rms_adaln: as sol_layer_norm_backward with x^ = x * rstd,
+ * rstd = 1 / sqrt(mean_c(x^2) + eps) computed again from x, n = x^ * gamma,
+ * and dx = rstd * (g - x^ * mean_c(g * x^)) + dres.
+ *
+ *   scale         [B, 2, D], as given to the forward call (required).
+ *   gamma         [D], or NULL if the forward call had none.
+ *   eps           that of the forward call.
+ *   other arguments as for sol_layer_norm_backward.
+ */
+sol_status sol_rms_adaln_backward(const void *dy, const void *x,
+                                  const void *scale, const void *gamma,
+                                  const void *dres, void *dx, float *dscale,
+                                  float *dshift, float *dgamma, int64_t B,
+                                  int64_t L, int64_t n_video, int64_t D,
+                                  float eps, void *workspace,
+                                  size_t workspace_bytes, sol_dtype dtype,
+                                  sol_stream_t stream);
+
+/* Workspace bytes of the two norm gradients (a pure function of its
+ * arguments; 0 for arguments out of range). */
+size_t sol_norm_backward_workspace_bytes(int64_t B, int64_t L, int64_t D);
+
+/*
+ * Dropout in front of the AdaLN-gated residual.  For element e of [B, L, D]
+ * (e = (b*L + r)*D + c) in a row of sample b with modality m:
+ *
+ *   out[e] = h[e] + gate[b][m][c] * (keep_e ? branch[e] / (1 - p) : 0)
+ *
+ * keep_e: word e mod 4 of the Philox4x32-10 generator (Salmon et al., 2011)
+ * at counter (e / 4, offset + site), key seed, both 64-bit words low half
+ * first, is at least round(p * 2^32).  The mask is a function of (seed,
+ * offset + site, e, p) and is never stored: the backward call computes it
+ * again.  A dropped element adds 0 whatever branch holds there.
+ *
+ *   h             [B, L, D] device, or NULL for 0.
+ *   branch        [B, L, D] device.
+ *   gate          [B, 2, D] device, or NULL for 1.
+ *   out           [B, L, D]; may equal h or branch (in place).
+ *   rng           device, two uint64: seed, offset; 8-byte aligned; read by the
+ *                 kernel, so that a captured graph draws another mask when its
+ *                 owner changes them between replays.  May be NULL if p = 0.
+ *   site          added to offset (modulo 2^64): one number per dropout of a
+ *                 step keeps their masks apart.
+ *   p             0 <= p <= 1 (p = 0 keeps all: sol_gate_residual; p = 1 drops
+ *                 all).
+ *   n_video, D    as for sol_rms_adaln (same D limit).
+ */
+sol_status sol_dropout_residual(const void *h, const void *branch,
+                                const void *gate, void *out,
+                                const uint64_t *rng, uint64_t site, float p,
+                                int64_t B, int64_t L, int64_t n_video,
+                                int64_t D, sol_dtype dtype,
+                                sol_stream_t stream);
+
+/*
+ * Gradient of sol_dropout_residual (dh is dout itself):
+ *
+ *   dbranch[e]       = gate[b][m][c] * (keep_e ? dout[e] / (1 - p) : 0)
+ *   dgate[b][m][c]   = sum over the rows of (b, m) of
+ *                      keep_e ? dout[e] * branch[e] / (1 - p) : 0
+ *
+ *   dout          [B, L, D] device.
+ *   branch        [B, L, D] device, as given to the forward call; may be NULL
+ *                 if dgate is.
+ *   gate          [B, 2, D], or NULL if the forward call had none (then dgate
+ *                 must be NULL).
+ *   dbranch       [B, L, D]; may equal dout or branch (in place).
+ *   dgate         [B, 2, D] fp32, or NULL (not wanted).
+ *   rng, site, p  those of the forward call.
+ *   workspace     sol_dropout_backward_workspace_bytes; may be NULL if dgate
+ *                 is.
+ *   With dgate, B <= 32767.  p = 0 gives the gradient of sol_gate_residual.
+ */
+sol_status sol_dropout_residual_backward(
+    const void *dout, const void *branch, const void *gate, void *dbranch,
+    float *dgate, const uint64_t *rng, uint64_t site, float p, int64_t B,
+    int64_t L, int64_t n_video, int64_t D, void *workspace,
+    size_t workspace_bytes, sol_dtype dtype, sol_stream_t stream);
+
+/* Workspace bytes of sol_dropout_residual_backward (as
+ * sol_norm_backward_workspace_bytes). */
+size_t sol_dropout_backward_workspace_bytes(int64_t B, int64_t L, int64_t D);
+
+/*
+ * Rotary positions with several axes, at explicit position ids.
+ *
+ * A plan (host memory, plain data; sol_rope_plan_init fills it) says how the
+ * first rot_dim channels of a head are rotated: pair i turns by
+ * pos[axis[i]] * freq[i].  A caller may overwrite freq (scaled ladders) with
+ * any finite values.
+ */
+typedef struct sol_rope_plan {
+    int32_t head_dim;   /* channels of a head */
+    int32_t rot_dim;    /* even; the first rot_dim channels are rotated */
+    int32_t n_axes;     /* 1 .. 8 */
+    int32_t half_split; /* 0: pair i = channels (2i, 2i+1); 1: (i, i + rot_dim/2) */
+    uint8_t axis[128];  /* axis of pair i, i < rot_dim / 2 */
+    double freq[128];   /* radians per unit of position */
+} sol_rope_plan;
+
+/*
+ * Fill a plan.
+ *   sections       n_axes pair counts >= 0 whose sum is rot_dim / 2.
+ *   theta > 0.
+ *   per_axis_freq  0: freq[i] = theta^(-2i/rot_dim) over all pairs; 1: local
+ *                  pair j of an axis with s pairs has theta^(-j/s).
+ *   interleaved    0: the axes take consecutive blocks of pairs; 1: they take
+ *                  one pair each in turn, axis 0 first, an axis that has all
+ *                  of its pairs being passed over.
+ *   head_dim in 2 .. 256, 0 < rot_dim <= head_dim, rot_dim even.
+ */
+sol_status sol_rope_plan_init(sol_rope_plan *plan, int64_t head_dim,
+                              int64_t rot_dim, int64_t n_axes,
+                              const int64_t *sections, double theta,
+                              int per_axis_freq, int interleaved,
+                              int half_split);
+
+typedef enum sol_pos_type {
+    SOL_POS_I32 = 0,
+    SOL_POS_I64 = 1,
+    SOL_POS_F32 = 2
+} sol_pos_type;
+
+/* Position ids: axis a of row r of sample b is element a*stride_axis +
+ * b*stride_b + r.  stride_b = 0 shares one set of rows among the samples.
+ * Angles are exact to fp32 for |position| up to 2^31. */
+typedef struct sol_positions {
+    const void *data;   /* device, aligned to its element */
+    int32_t type;       /* sol_pos_type */
+    int32_t reserved;   /* must be 0 */
+    int64_t stride_axis;
+    int64_t stride_b;
+} sol_positions;
+
+/* Head vectors: channel c of head h of row r of sample b is element
+ * b*stride_b + r*stride_row + h*stride_head + c.  Strides are >= 0 and, like
+ * data, multiples of 16 bytes; those of an output must address distinct
+ * elements (not checked). */
+typedef struct sol_heads {
+    void *data;         /* device */
+    int64_t n_heads;    /* 1 .. 1024 */
+    int64_t stride_b;
+    int64_t stride_row;
+    int64_t stride_head;
+} sol_heads;
+
+/*
+ * Rotate q and k, each B x L rows of its own number of heads, optionally
+ * behind the per-head RMS norm of sol_qknorm_rope3d (qk_norm = 1):
+ *
+ *   n[c] = x[c] / sqrt(mean_c(x^2) + eps) * gamma[c]     (qk_norm; else n = x)
+ *   out  = n with pair (u, v) of channels i turned by phi = pos * freq:
+ *          (u cos phi - v sin phi, u sin phi + v cos phi)
+ *
+ *   k, k_out         may both be NULL (q alone).
+ *   q_out, k_out     may equal their input exactly (same data and strides, in
+ *                    place), else overlap no other argument.
+ *   gamma_q, gamma_k [head_dim] device, or NULL for 1; NULL without qk_norm.
+ *   head_dim         a multiple of 16 bytes of the element type, up to 256
+ *                    (bf16) / 128 (fp32) channels; with half_split rot_dim / 2
+ *                    a multiple of 16 bytes too (SOL_ERR_UNSUPPORTED else).
+ */
+sol_status sol_rope_axes(const sol_rope_plan *plan, const sol_positions *pos,
+                         const sol_heads *q, const sol_heads *k,
+                         const sol_heads *q_out, const sol_heads *k_out,
+                         const void *gamma_q, const void *gamma_k, int qk_norm,
+                         int64_t B, int64_t L, float eps, sol_dtype dtype,
+                         sol_stream_t stream);
+
+/*
+ * Gradient of sol_rope_axes: with g = dq_out (dk_out) rotated by -phi,
+ * without qk_norm dq = g; with it, per head, x^ = x * rstd:
+ *
+ *   dq     = rstd * (gamma * g - x^ * mean_c(x^ * gamma * g))
+ *   dgamma = sum over all rows and heads of g * x^
+ *
+ *   dq_out, dk_out   gradients of the outputs.
+ *   q, k             the forward call's inputs; NULL without qk_norm.
+ *   dq, dk           may equal dq_out or q (dk_out or k) exactly (in place),
+ *                    else overlap no other argument.
+ *   gamma_q, gamma_k, qk_norm, eps, plan, pos  those of the forward call.
+ *   dgamma_q, dgamma_k  [head_dim] fp32; each may be NULL (not wanted), NULL
+ *                    without qk_norm.
+ *   workspace        sol_rope_backward_workspace_bytes; may be NULL when no
+ *                    dgamma is wanted.
+ *   dk_out, k, dk    all NULL for q alone.
+ */
+sol_status sol_rope_axes_backward(
+    const sol_rope_plan *plan, const sol_positions *pos,
+    const sol_heads *dq_out, const sol_heads *dk_out, const sol_heads *q,
+    const sol_heads *k, const sol_heads *dq, const sol_heads *dk,
+    const void *gamma_q, const void *gamma_k, float *dgamma_q, float *dgamma_k,
+    int qk_norm, int64_t B, int64_t L, float eps, void *workspace,
+    size_t workspace_bytes, sol_dtype dtype, sol_stream_t stream);
+
+/* Workspace bytes of sol_rope_axes_backward with a dgamma (0 for a head_dim
+ * out of range). */
+size_t sol_rope_backward_workspace_bytes(int64_t head_dim);
+
 /* Static, human-readable name of a status code. */
 const char *sol_status_string(sol_status status);
 
@@ -453,7 +727,9 @@ const char *sol_last_error(void);
 /* ABI version, (major << 16) | minor.  2.0: sol_qk_layout gained
  * per_axis_freq, reserved, v_out and v_scale (a larger struct; callers built
  * against 1.x must be rebuilt).  2.1: the rotary table (sol_rope_table,
- * sol_qknorm_rope3d_tab, sol_qknorm_rope3d_ex_tab). */
+ * sol_qknorm_rope3d_tab, sol_qknorm_rope3d_ex_tab).  2.2: the training
+ * operators (layer norm, norm gradients, dropout, rotary positions with
+ * several axes). */
 int sol_version(void);
 
 #ifdef __cplusplus

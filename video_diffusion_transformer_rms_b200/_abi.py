@@ -24,6 +24,11 @@ SOL_ERR_CUDA = 4
 SOL_F32 = 0
 SOL_BF16 = 1
 
+SOL_POS_I32 = 0
+SOL_POS_I64 = 1
+SOL_POS_F32 = 2
+
+
 class QkLayout(ctypes.Structure):
     """sol_qk_layout of include/sol.h."""
     _fields_ = [("stride_b", ctypes.c_int64), ("stride_row", ctypes.c_int64),
@@ -41,6 +46,27 @@ class RopeTable(ctypes.Structure):
                 ("head_dim", ctypes.c_int64), ("sec_t", ctypes.c_int64),
                 ("sec_h", ctypes.c_int64), ("sec_w", ctypes.c_int64),
                 ("theta", ctypes.c_float), ("per_axis_freq", ctypes.c_int32)]
+
+
+class RopePlan(ctypes.Structure):
+    """sol_rope_plan of include/sol.h: axis and frequency of every rotary pair."""
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("half_split", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * 128), ("freq", ctypes.c_double * 128)]
+
+
+class Positions(ctypes.Structure):
+    """sol_positions of include/sol.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("type", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("stride_axis", ctypes.c_int64),
+                ("stride_b", ctypes.c_int64)]
+
+
+class Heads(ctypes.Structure):
+    """sol_heads of include/sol.h: head vectors of [B, L] rows, any strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("n_heads", ctypes.c_int64),
+                ("stride_b", ctypes.c_int64), ("stride_row", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -102,6 +128,32 @@ def lib() -> ctypes.CDLL:
                                                ctypes.POINTER(RopeTable), i64, i64, i64, i64,
                                                i64, i64, f, i, p]
         L.sol_qknorm_rope3d_ex_tab.restype = i
+        sz, u64, plan, pos, hv = (ctypes.c_size_t, ctypes.c_uint64, ctypes.POINTER(RopePlan),
+                                  ctypes.POINTER(Positions), ctypes.POINTER(Heads))
+        L.sol_layer_norm.argtypes = [p] * 8 + [i64] * 4 + [f, i, p]
+        L.sol_layer_norm.restype = i
+        L.sol_layer_norm_backward.argtypes = [p] * 13 + [i64] * 4 + [p, sz, i, p]
+        L.sol_layer_norm_backward.restype = i
+        L.sol_rms_adaln_backward.argtypes = [p] * 9 + [i64] * 4 + [f, p, sz, i, p]
+        L.sol_rms_adaln_backward.restype = i
+        L.sol_norm_backward_workspace_bytes.argtypes = [i64, i64, i64]
+        L.sol_norm_backward_workspace_bytes.restype = sz
+        L.sol_dropout_residual.argtypes = [p] * 5 + [u64, f] + [i64] * 4 + [i, p]
+        L.sol_dropout_residual.restype = i
+        L.sol_dropout_residual_backward.argtypes = [p] * 6 + [u64, f] + [i64] * 4 + [p, sz, i, p]
+        L.sol_dropout_residual_backward.restype = i
+        L.sol_dropout_backward_workspace_bytes.argtypes = [i64, i64, i64]
+        L.sol_dropout_backward_workspace_bytes.restype = sz
+        L.sol_rope_plan_init.argtypes = [plan, i64, i64, i64, ctypes.POINTER(i64),
+                                         ctypes.c_double, i, i, i]
+        L.sol_rope_plan_init.restype = i
+        L.sol_rope_axes.argtypes = [plan, pos, hv, hv, hv, hv, p, p, i, i64, i64, f, i, p]
+        L.sol_rope_axes.restype = i
+        L.sol_rope_axes_backward.argtypes = [plan, pos, hv, hv, hv, hv, hv, hv, p, p, p, p, i,
+                                             i64, i64, f, p, sz, i, p]
+        L.sol_rope_axes_backward.restype = i
+        L.sol_rope_backward_workspace_bytes.argtypes = [i64]
+        L.sol_rope_backward_workspace_bytes.restype = sz
         L.sol_status_string.argtypes = [i]
         L.sol_status_string.restype = ctypes.c_char_p
         L.sol_last_error.argtypes = []
@@ -213,6 +265,78 @@ def sol_gemm_gelu(A, B, bias, C, M, N, K, workspace, workspace_bytes, stream) ->
 
 def sol_gemm_gelu_workspace_bytes(M, N, K) -> int:
     return lib().sol_gemm_gelu_workspace_bytes(M, N, K)
+
+
+def sol_layer_norm(x, y, mean, rstd, gamma, beta, scale, shift, B, L, n_video, D, eps, dtype,
+                   stream) -> int:
+    return lib().sol_layer_norm(x, y, mean, rstd, gamma, beta, scale, shift, B, L, n_video, D,
+                                eps, dtype, stream)
+
+
+def sol_layer_norm_backward(dy, x, mean, rstd, gamma, beta, scale, dres, dx, dgamma, dbeta,
+                            dscale, dshift, B, L, n_video, D, workspace, workspace_bytes, dtype,
+                            stream) -> int:
+    return lib().sol_layer_norm_backward(dy, x, mean, rstd, gamma, beta, scale, dres, dx, dgamma,
+                                         dbeta, dscale, dshift, B, L, n_video, D, workspace,
+                                         workspace_bytes, dtype, stream)
+
+
+def sol_rms_adaln_backward(dy, x, scale, gamma, dres, dx, dscale, dshift, dgamma, B, L, n_video,
+                           D, eps, workspace, workspace_bytes, dtype, stream) -> int:
+    return lib().sol_rms_adaln_backward(dy, x, scale, gamma, dres, dx, dscale, dshift, dgamma, B,
+                                        L, n_video, D, eps, workspace, workspace_bytes, dtype,
+                                        stream)
+
+
+def sol_norm_backward_workspace_bytes(B, L, D) -> int:
+    return lib().sol_norm_backward_workspace_bytes(B, L, D)
+
+
+def sol_dropout_residual(h, branch, gate, out, rng, site, p, B, L, n_video, D, dtype,
+                         stream) -> int:
+    return lib().sol_dropout_residual(h, branch, gate, out, rng, site, p, B, L, n_video, D, dtype,
+                                      stream)
+
+
+def sol_dropout_residual_backward(dout, branch, gate, dbranch, dgate, rng, site, p, B, L,
+                                  n_video, D, workspace, workspace_bytes, dtype, stream) -> int:
+    return lib().sol_dropout_residual_backward(dout, branch, gate, dbranch, dgate, rng, site, p,
+                                               B, L, n_video, D, workspace, workspace_bytes,
+                                               dtype, stream)
+
+
+def sol_dropout_backward_workspace_bytes(B, L, D) -> int:
+    return lib().sol_dropout_backward_workspace_bytes(B, L, D)
+
+
+def sol_rope_plan_init(plan, head_dim, rot_dim, n_axes, sections, theta, per_axis_freq,
+                       interleaved, half_split) -> int:
+    """plan: a RopePlan to fill; sections: a sequence of pair counts (or None,
+    which the library rejects, as it does a plan of None)."""
+    sec = None if sections is None else (ctypes.c_int64 * len(sections))(*sections)
+    return lib().sol_rope_plan_init(_ref(plan), head_dim, rot_dim, n_axes, sec, theta,
+                                    per_axis_freq, interleaved, half_split)
+
+
+def sol_rope_axes(plan, pos, q, k, q_out, k_out, gamma_q, gamma_k, qk_norm, B, L, eps, dtype,
+                  stream) -> int:
+    """plan: a RopePlan; pos: Positions; q .. k_out: Heads, or None."""
+    return lib().sol_rope_axes(_ref(plan), _ref(pos), _ref(q), _ref(k), _ref(q_out), _ref(k_out),
+                               gamma_q, gamma_k, qk_norm, B, L, eps, dtype, stream)
+
+
+def sol_rope_axes_backward(plan, pos, dq_out, dk_out, q, k, dq, dk, gamma_q, gamma_k, dgamma_q,
+                           dgamma_k, qk_norm, B, L, eps, workspace, workspace_bytes, dtype,
+                           stream) -> int:
+    """plan: a RopePlan; pos: Positions; dq_out .. dk: Heads, or None."""
+    return lib().sol_rope_axes_backward(_ref(plan), _ref(pos), _ref(dq_out), _ref(dk_out),
+                                        _ref(q), _ref(k), _ref(dq), _ref(dk), gamma_q, gamma_k,
+                                        dgamma_q, dgamma_k, qk_norm, B, L, eps, workspace,
+                                        workspace_bytes, dtype, stream)
+
+
+def sol_rope_backward_workspace_bytes(head_dim) -> int:
+    return lib().sol_rope_backward_workspace_bytes(head_dim)
 
 
 def sol_status_string(status: int) -> str:

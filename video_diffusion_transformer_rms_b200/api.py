@@ -3,7 +3,8 @@ their pointers, shapes and the current stream to libsol.  Marshalling only
 (PyTorch allocates outputs when the caller does not pass them); the
 arithmetic runs in libsol's kernels.
 """
-from typing import Optional, Sequence, Tuple
+import contextlib
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -312,3 +313,376 @@ def gemm_gelu(A: torch.Tensor, B: torch.Tensor, bias: Optional[torch.Tensor] = N
     _abi.check(_abi.sol_gemm_gelu(_ptr(A), _ptr(B), _ptr(bias), _ptr(C), M, N, K, _ptr(ws),
                                   need, _stream(stream)))
     return C
+
+
+# ---------------------------------------------------------------------------
+# training operators
+# ---------------------------------------------------------------------------
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
+    """The context a call on `t` runs in: t's device is current, and `stream`,
+    where one is given, is the current stream, so that outputs and workspaces
+    allocated inside belong to the stream that uses them."""
+    if not t.is_cuda:
+        raise ValueError("libsol takes CUDA tensors")
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the inputs on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return _NO_CONTEXT
+
+
+def _workspace(given: Optional[torch.Tensor], need: int, like: torch.Tensor) -> torch.Tensor:
+    if given is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+    _expect(given, given.shape, "workspace", like)
+    return given
+
+
+def _rows3(x: torch.Tensor, n_video: Optional[int], name: str):
+    if x.dim() != 3 or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [B, L, D] tensor")
+    B, L, D = x.shape
+    return B, L, D, L if n_video is None else n_video
+
+
+def _fp32(shape, like: torch.Tensor) -> torch.Tensor:
+    return torch.empty(shape, dtype=torch.float32, device=like.device)
+
+
+def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+               beta: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+               shift: Optional[torch.Tensor] = None, n_video: Optional[int] = None,
+               eps: float = 1e-6, stats: bool = True, out: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None
+               ) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """y = (LayerNorm(x) * gamma + beta) * (1 + scale[b, m]) + shift[b, m];
+    x: [B, L, D], gamma/beta: [D] or None, scale/shift: [B, 2, D] or both
+    None.  Returns (y, mean, rstd); the statistics, fp32 [B, L], are what
+    layer_norm_backward takes, and None with stats=False."""
+    B, L, D, nv = _rows3(x, n_video, "x")
+    for t, shape, name in ((gamma, (D,), "gamma"), (beta, (D,), "beta"),
+                           (scale, (B, 2, D), "scale"), (shift, (B, 2, D), "shift"),
+                           (out, (B, L, D), "out")):
+        _expect(t, shape, name, x)
+    dt = _dtype(x, gamma, beta, scale, shift, out)
+    with _on(x, stream):
+        y = torch.empty_like(x) if out is None else out
+        mean = _fp32((B, L), x) if stats else None
+        rstd = _fp32((B, L), x) if stats else None
+        _abi.check(_abi.sol_layer_norm(_ptr(x), _ptr(y), _ptr(mean), _ptr(rstd), _ptr(gamma),
+                                       _ptr(beta), _ptr(scale), _ptr(shift), B, L, nv, D, eps,
+                                       dt, _stream(None)))
+    return y, mean, rstd
+
+
+class NormGrads(NamedTuple):
+    """Gradients of layer_norm; None where the input was not given.  Those of
+    vectors are fp32."""
+    dx: torch.Tensor
+    dgamma: Optional[torch.Tensor]
+    dbeta: Optional[torch.Tensor]
+    dscale: Optional[torch.Tensor]
+    dshift: Optional[torch.Tensor]
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
+                        rstd: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+                        beta: Optional[torch.Tensor] = None,
+                        scale: Optional[torch.Tensor] = None, n_video: Optional[int] = None,
+                        dres: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> NormGrads:
+    """Gradients of layer_norm(x, gamma, beta, scale, shift) for dy.  mean and
+    rstd are those the forward call returned; dres, a gradient of x's shape, is
+    added to dx.  dx may be dy, x or dres (in place).  The workspace
+    (sol_norm_backward_workspace_bytes) is allocated by PyTorch unless given."""
+    B, L, D, nv = _rows3(x, n_video, "x")
+    for t, shape, name in ((dy, (B, L, D), "dy"), (mean, (B, L), "mean"), (rstd, (B, L), "rstd"),
+                           (gamma, (D,), "gamma"), (beta, (D,), "beta"),
+                           (scale, (B, 2, D), "scale"), (dres, (B, L, D), "dres"),
+                           (dx, (B, L, D), "dx")):
+        _expect(t, shape, name, x)
+    if mean.dtype != torch.float32 or rstd.dtype != torch.float32:
+        raise TypeError("mean and rstd must be float32")
+    dt = _dtype(x, dy, gamma, beta, scale, dres, dx)
+    with _on(x, stream):
+        d = torch.empty_like(x) if dx is None else dx
+        dgamma = None if gamma is None else _fp32((D,), x)
+        dbeta = None if beta is None else _fp32((D,), x)
+        dscale = None if scale is None else _fp32((B, 2, D), x)
+        dshift = None if scale is None else _fp32((B, 2, D), x)
+        ws = _workspace(workspace, _abi.sol_norm_backward_workspace_bytes(B, L, D), x)
+        _abi.check(_abi.sol_layer_norm_backward(
+            _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(beta), _ptr(scale),
+            _ptr(dres), _ptr(d), _ptr(dgamma), _ptr(dbeta), _ptr(dscale), _ptr(dshift), B, L, nv,
+            D, _ptr(ws), ws.numel() * ws.element_size(), dt, _stream(None)))
+    return NormGrads(d, dgamma, dbeta, dscale, dshift)
+
+
+def rms_adaln_backward(dy: torch.Tensor, x: torch.Tensor, scale: torch.Tensor, n_video: int,
+                       gamma: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                       dres: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None
+                       ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor,
+                                  Optional[torch.Tensor]]:
+    """Gradients (dx, dscale, dshift, dgamma) of rms_adaln(x, scale, shift,
+    n_video, gamma, eps) for dy; those of vectors fp32, dgamma None without
+    gamma.  dres, dx and workspace as for layer_norm_backward."""
+    B, L, D, nv = _rows3(x, n_video, "x")
+    for t, shape, name in ((dy, (B, L, D), "dy"), (scale, (B, 2, D), "scale"),
+                           (gamma, (D,), "gamma"), (dres, (B, L, D), "dres"),
+                           (dx, (B, L, D), "dx")):
+        _expect(t, shape, name, x)
+    dt = _dtype(x, dy, scale, gamma, dres, dx)
+    with _on(x, stream):
+        d = torch.empty_like(x) if dx is None else dx
+        dscale, dshift = _fp32((B, 2, D), x), _fp32((B, 2, D), x)
+        dgamma = None if gamma is None else _fp32((D,), x)
+        ws = _workspace(workspace, _abi.sol_norm_backward_workspace_bytes(B, L, D), x)
+        _abi.check(_abi.sol_rms_adaln_backward(
+            _ptr(dy), _ptr(x), _ptr(scale), _ptr(gamma), _ptr(dres), _ptr(d), _ptr(dscale),
+            _ptr(dshift), _ptr(dgamma), B, L, nv, D, eps, _ptr(ws),
+            ws.numel() * ws.element_size(), dt, _stream(None)))
+    return d, dscale, dshift, dgamma
+
+
+def _check_rng(rng: Optional[torch.Tensor], p: float, like: torch.Tensor):
+    if rng is None:
+        if p != 0:
+            raise ValueError("rng is needed with p > 0")
+        return
+    _expect(rng, (2,), "rng", like)
+    if rng.dtype not in (torch.int64, torch.uint64):
+        raise TypeError("rng must be int64 or uint64: (seed, offset)")
+
+
+def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], site: int = 0,
+            out: Optional[torch.Tensor] = None,
+            stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """x / (1 - p) where the generator keeps the element, else 0; x: any
+    contiguous tensor.  The mask is a function of (seed, offset + site, the
+    element's index, p), with rng = (seed, offset) two int64 on x's device: the
+    gradient is dropout(dout, p, rng, site)."""
+    if x.dim() < 1 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous tensor")
+    _expect(out, x.shape, "out", x)
+    _check_rng(rng, p, x)
+    D = x.shape[-1]
+    rows = x.numel() // D if D else 0
+    dt = _dtype(x, out)
+    with _on(x, stream):
+        o = torch.empty_like(x) if out is None else out
+        if x.numel():
+            _abi.check(_abi.sol_dropout_residual(None, _ptr(x), None, _ptr(o), _ptr(rng),
+                                                 site % 2**64, p, 1, rows, rows, D, dt,
+                                                 _stream(None)))
+    return o
+
+
+def dropout_residual(h: Optional[torch.Tensor], branch: torch.Tensor,
+                     gate: Optional[torch.Tensor], n_video: Optional[int], p: float,
+                     rng: Optional[torch.Tensor], site: int = 0,
+                     out: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """out = h + gate[b, m] * dropout(branch); h/branch: [B, L, D], gate:
+    [B, 2, D] (None for 1; h None for 0).  rng and site as for dropout; no mask
+    is stored.  out may be h or branch (in place)."""
+    B, L, D, nv = _rows3(branch, n_video, "branch")
+    for t, shape, name in ((h, (B, L, D), "h"), (gate, (B, 2, D), "gate"),
+                           (out, (B, L, D), "out")):
+        _expect(t, shape, name, branch)
+    _check_rng(rng, p, branch)
+    dt = _dtype(branch, h, gate, out)
+    with _on(branch, stream):
+        o = torch.empty_like(branch) if out is None else out
+        _abi.check(_abi.sol_dropout_residual(_ptr(h), _ptr(branch), _ptr(gate), _ptr(o),
+                                             _ptr(rng), site % 2**64, p, B, L, nv, D, dt,
+                                             _stream(None)))
+    return o
+
+
+def dropout_residual_backward(dout: torch.Tensor, branch: Optional[torch.Tensor],
+                              gate: Optional[torch.Tensor], n_video: Optional[int], p: float,
+                              rng: Optional[torch.Tensor], site: int = 0,
+                              dbranch: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None,
+                              stream: Optional[torch.cuda.Stream] = None
+                              ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gradients (dbranch, dgate) of dropout_residual for dout (that of h is
+    dout itself), the mask computed again from rng, site and p; dgate is fp32,
+    and None without gate (branch may be None then).  p = 0 gives the gradients
+    of gate_residual.  dbranch may be dout or branch (in place)."""
+    B, L, D, nv = _rows3(dout, n_video, "dout")
+    if gate is not None and branch is None:
+        raise ValueError("branch is needed for the gradient of gate")
+    for t, shape, name in ((branch, (B, L, D), "branch"), (gate, (B, 2, D), "gate"),
+                           (dbranch, (B, L, D), "dbranch")):
+        _expect(t, shape, name, dout)
+    _check_rng(rng, p, dout)
+    dt = _dtype(dout, branch, gate, dbranch)
+    with _on(dout, stream):
+        d = torch.empty_like(dout) if dbranch is None else dbranch
+        dgate = ws = None
+        if gate is not None:
+            dgate = _fp32((B, 2, D), dout)
+            ws = _workspace(workspace, _abi.sol_dropout_backward_workspace_bytes(B, L, D), dout)
+        _abi.check(_abi.sol_dropout_residual_backward(
+            _ptr(dout), _ptr(branch), _ptr(gate), _ptr(d), _ptr(dgate), _ptr(rng), site % 2**64,
+            p, B, L, nv, D, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), dt,
+            _stream(None)))
+    return d, dgate
+
+
+class RopeAxes:
+    """How the heads of rope_axes are rotated (sol_rope_plan): `sections` gives
+    each position axis its number of rotary pairs, in consecutive blocks or,
+    with interleaved=True, one pair each in turn; the first
+    rot_dim = 2 * sum(sections) channels of a head are rotated.  per_axis_freq
+    gives every axis a frequency ladder of its own; half_split pairs channel i
+    with i + rot_dim / 2.  Build it once; `desc.freq` may be rescaled."""
+
+    def __init__(self, head_dim: int, sections: Sequence[int], theta: float = 10000.0,
+                 per_axis_freq: bool = False, interleaved: bool = False,
+                 half_split: bool = False):
+        self.head_dim, self.n_axes = head_dim, len(sections)
+        self.desc = _abi.RopePlan()
+        _abi.check(_abi.sol_rope_plan_init(self.desc, head_dim, 2 * sum(sections),
+                                           len(sections), sections, theta,
+                                           int(bool(per_axis_freq)), int(bool(interleaved)),
+                                           int(bool(half_split))))
+
+
+_POS = {torch.int32: _abi.SOL_POS_I32, torch.int64: _abi.SOL_POS_I64,
+        torch.float32: _abi.SOL_POS_F32}
+
+
+def _strides(t: torch.Tensor):
+    return [0 if n == 1 else s for n, s in zip(t.shape, t.stride())]
+
+
+def _heads(t: Optional[torch.Tensor], B: int, L: int, hd: int, name: str, like: torch.Tensor,
+           heads: Optional[int] = None, written: bool = False) -> Optional[_abi.Heads]:
+    if t is None:
+        return None
+    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != L or t.shape[3] != hd or (
+            heads is not None and t.shape[2] != heads) or (hd > 1 and t.stride(3) != 1):
+        raise ValueError(f"{name} must be [{B}, {L}, {'heads' if heads is None else heads}, {hd}] "
+                         f"with unit channel stride, got {tuple(t.shape)}, strides {t.stride()}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, q on {like.device}")
+    sb, sr, sh, _ = _strides(t)
+    if written and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        raise ValueError(f"{name} must not be an expanded tensor")
+    return _abi.Heads(_ptr(t), t.shape[2], sb, sr, sh)
+
+
+def _positions(pos: torch.Tensor, B: int, L: int, n_axes: int, like: torch.Tensor):
+    if pos.dtype not in _POS:
+        raise TypeError("pos must be int32, int64 or float32")
+    if tuple(pos.shape) not in ((n_axes, B, L), (n_axes, L)) or (L > 1 and pos.stride(-1) != 1):
+        raise ValueError(f"pos must be [{n_axes}, {B}, {L}] or [{n_axes}, {L}] with unit row "
+                         f"stride, got {tuple(pos.shape)}")
+    if pos.device != like.device:
+        raise ValueError(f"pos is on {pos.device}, q on {like.device}")
+    s = _strides(pos)
+    return _abi.Positions(_ptr(pos), _POS[pos.dtype], 0, s[0], s[1] if pos.dim() == 3 else 0)
+
+
+def _rope_shapes(q, k, plan, what):
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError(f"{what} must be [B, L, heads, head_dim]")
+    B, L, _, hd = q.shape
+    if hd != plan.head_dim:
+        raise ValueError(f"{what} has heads of {hd}, the plan of {plan.head_dim}")
+    return B, L, hd
+
+
+def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, plan: RopeAxes,
+              gamma_q: Optional[torch.Tensor] = None, gamma_k: Optional[torch.Tensor] = None,
+              qk_norm: bool = False, eps: float = 1e-6, q_out: Optional[torch.Tensor] = None,
+              k_out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+              ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Rotate q [B, L, Hq, hd] and k [B, L, Hk, hd] (any strides: columns of a
+    merged projection, a transposed [B, H, L, hd]; k may be None) at positions
+    pos [n_axes, B, L], or [n_axes, L] for all samples (int32, int64 or
+    float32), behind a per-head RMS norm with qk_norm=True (gamma_q/gamma_k
+    [hd] or None).  Returns (q_out, k_out); pass q_out=q, k_out=k to rotate in
+    place."""
+    B, L, hd = _rope_shapes(q, k, plan, "q")
+    for t, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
+        _expect(t, (hd,), name, q)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    dt = _dtype(q, k, gamma_q, gamma_k, q_out, k_out)
+    with _on(q, stream):
+        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        ko = k_out
+        if k is not None and k_out is None:
+            ko = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        Hk = None if k is None else k.shape[2]
+        _abi.check(_abi.sol_rope_axes(
+            plan.desc, _positions(pos, B, L, plan.n_axes, q), _heads(q, B, L, hd, "q", q),
+            _heads(k, B, L, hd, "k", q), _heads(qo, B, L, hd, "q_out", q, q.shape[2], True),
+            _heads(ko, B, L, hd, "k_out", q, Hk, True), _ptr(gamma_q), _ptr(gamma_k),
+            int(bool(qk_norm)), B, L, eps, dt, _stream(None)))
+    return qo, ko
+
+
+class RopeGrads(NamedTuple):
+    """Gradients of rope_axes; None where the input was not given.  dgamma_q and
+    dgamma_k are fp32."""
+    dq: torch.Tensor
+    dk: Optional[torch.Tensor]
+    dgamma_q: Optional[torch.Tensor]
+    dgamma_k: Optional[torch.Tensor]
+
+
+def rope_axes_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], pos: torch.Tensor,
+                       plan: RopeAxes, q: Optional[torch.Tensor] = None,
+                       k: Optional[torch.Tensor] = None, gamma_q: Optional[torch.Tensor] = None,
+                       gamma_k: Optional[torch.Tensor] = None, qk_norm: bool = False,
+                       eps: float = 1e-6, dq: Optional[torch.Tensor] = None,
+                       dk: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> RopeGrads:
+    """Gradients of rope_axes(q, k, pos, plan, gamma_q, gamma_k, qk_norm, eps)
+    for (dq_out, dk_out).  q and k are read with qk_norm only.  dq and dk may
+    be given with any strides (columns of a merged gradient) and may be dq_out
+    and dk_out, or q and k (in place)."""
+    B, L, hd = _rope_shapes(dq_out, dk_out, plan, "dq_out")
+    for t, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
+        _expect(t, (hd,), name, dq_out)
+    if qk_norm and (q is None or (k is None) != (dk_out is None)):
+        raise ValueError("qk_norm needs q, and k together with dk_out")
+    if dk_out is None and dk is not None:
+        raise ValueError("dk without dk_out")
+    if not qk_norm:
+        q = k = None
+    dt = _dtype(dq_out, dk_out, q, k, gamma_q, gamma_k, dq, dk)
+    like = dq_out
+    Hq, Hk = dq_out.shape[2], None if dk_out is None else dk_out.shape[2]
+    with _on(like, stream):
+        gq = torch.empty(dq_out.shape, dtype=like.dtype, device=like.device) if dq is None else dq
+        gk = dk
+        if dk_out is not None and dk is None:
+            gk = torch.empty(dk_out.shape, dtype=like.dtype, device=like.device)
+        dgq = None if gamma_q is None else _fp32((hd,), like)
+        dgk = None if gamma_k is None else _fp32((hd,), like)
+        ws = None
+        if dgq is not None or dgk is not None:
+            ws = _workspace(workspace, _abi.sol_rope_backward_workspace_bytes(hd), like)
+        _abi.check(_abi.sol_rope_axes_backward(
+            plan.desc, _positions(pos, B, L, plan.n_axes, like),
+            _heads(dq_out, B, L, hd, "dq_out", like), _heads(dk_out, B, L, hd, "dk_out", like),
+            _heads(q, B, L, hd, "q", like, Hq), _heads(k, B, L, hd, "k", like, Hk),
+            _heads(gq, B, L, hd, "dq", like, Hq, True), _heads(gk, B, L, hd, "dk", like, Hk, True),
+            _ptr(gamma_q), _ptr(gamma_k), _ptr(dgq), _ptr(dgk), int(bool(qk_norm)), B, L, eps,
+            _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), dt, _stream(None)))
+    return RopeGrads(gq, gk, dgq, dgk)

@@ -24,10 +24,13 @@ SOURCES = ["sol_abi.cu", "rms_adaln.cu", "gate_residual.cu", "qknorm_rope3d_bf16
            "qknorm_rope3d_f32.cu", "qknorm_rope3d_tab_bf16.cu", "qknorm_rope3d_tab_f32.cu",
            "qknorm_rope3d_ex_bf16.cu", "qknorm_rope3d_ex_int8.cu", "qknorm_rope3d_ex_tab_bf16.cu",
            "qknorm_rope3d_ex_tab_int8.cu", "residual_change.cu", "quantize_heads.cu",
-           "rope_table.cu", "gemm_gelu.cu"]
+           "rope_table.cu", "gemm_gelu.cu", "sol_abi_train.cu", "layer_norm.cu",
+           "norm_backward.cu", "segment_sums.cu", "dropout_residual.cu", "rope_axes_bf16.cu",
+           "rope_axes_f32.cu"]
 # sources built against the CUTLASS / CuTe headers (the sm100 GEMM templates)
 CUTLASS_SOURCES = {"gemm_gelu.cu"}
-HEADERS = ["sol_device.cuh", "sol_launch.h", "qknorm_rope3d.cuh", "qknorm_rope3d_ex.cuh"]
+HEADERS = ["sol_device.cuh", "sol_launch.h", "sol_check.h", "sol_train.h", "segment_sums.cuh",
+           "qknorm_rope3d.cuh", "qknorm_rope3d_ex.cuh", "rope_axes.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

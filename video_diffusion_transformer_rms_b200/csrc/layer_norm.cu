@@ -1,0 +1,292 @@
+// Layer norm with optional weight, bias and adaptive modulation:
+//   n = (x - mean) * rstd * gamma + beta,  rstd = 1 / sqrt(var + eps),
+//   y = n * (1 + scale[b][m]) + shift[b][m]
+// per token row, m = video/audio modality of the row.  Per channel this is
+// y = (x - mean) * rstd * fac + off with fac = gamma * (1 + scale) and
+// off = beta * (1 + scale) + shift, both kept in fp32 registers and rebuilt
+// only when a CTA crosses a modality or sample boundary.
+//
+// The same persistent cp.async ring as RMS-AdaLN: chunks of rows dealt
+// round-robin over the CTAs, R rows per iteration, compile-time CTA size and
+// vectors per thread.
+//
+// Statistics in one barrier: each warp takes the mean of its own slice of the
+// row and the sum of squares about it, both from registers, and the warps'
+// (mean, M2) pairs are combined exactly,
+//   mean = sum n_w mean_w / D,  M2 = sum M2_w + n_w (mean_w - mean)^2,
+// so a row whose mean is large against its spread loses no digits, as
+// mean(x^2) - mean^2 would.
+//
+// Bound by HBM: x read, y written, 2*D*esize bytes per row.
+#include "sol_device.cuh"
+#include "sol_train.h"
+
+namespace sol {
+namespace {
+
+template <typename T, int NT, int VPT, int R, int S, int K>
+__global__ void __launch_bounds__(NT) layer_norm_kernel(const LnArgs a) {
+  static_assert(K % R == 0, "an iteration's rows must lie in one chunk");
+  using IO = Io<T>;
+  constexpr int P = IO::E / 2;
+  constexpr int NW = NT / 32;
+  extern __shared__ __align__(16) unsigned char smem[];
+  float2 *red = reinterpret_cast<float2 *>(smem);                   // [2][R][NW]: mean_w, M2_w
+  uint4 *ring = reinterpret_cast<uint4 *>(smem + 2 * R * NW * 8);  // [S][R][VPT][NT]
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 31;
+  const int warp = tid >> 5;
+  const int64_t row_bytes = static_cast<int64_t>(a.nvec) * 16;
+  const float inv_D = 1.f / static_cast<float>(a.D);
+
+  bool ok[VPT];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) ok[k] = k * NT + tid < a.nvec;
+  // elements of a row that warp w holds
+  auto warp_elems = [&](int w) -> float {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      int m = a.nvec - k * NT - w * 32;
+      m = m < 0 ? 0 : (m > 32 ? 32 : m);
+      n += m;
+    }
+    return static_cast<float>(n * IO::E);
+  };
+  const float nw_mine = warp_elems(warp);
+  const float inv_nw = nw_mine > 0.f ? 1.f / nw_mine : 0.f;
+
+  RowOrder<K, R> ro;
+  ro.init(a.rows);
+  const int count = ro.count;
+  const int iters = (count + R - 1) / R;
+  const unsigned char *xc = static_cast<const unsigned char *>(a.x);
+  unsigned char *yc = static_cast<unsigned char *>(a.y);
+
+  auto slot = [&](int s, int q, int k) -> uint4 * {
+    return &ring[((s * R + q) * VPT + k) * NT + tid];
+  };
+  auto issue = [&](int it, int s) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const int j = it * R + q;
+      if (j < count) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(xc + ro.row(j) * row_bytes) + tid;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+          if (ok[k]) cp_async16(slot(s, q, k), src + k * NT);
+      }
+    }
+    cp_async_commit();
+  };
+
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) issue(s, s);
+
+  float2 fac[VPT][P], off[VPT][P];
+  int key = -1;
+  int cons = 0;
+  int buf = 0;
+  TokenCursor cur;
+
+  auto load_vectors = [&]() {
+    const int64_t koff = static_cast<int64_t>(key) * a.nvec + tid;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      if (ok[k]) {
+#pragma unroll
+        for (int m = 0; m < P; ++m) {
+          fac[k][m] = splat2(1.f);
+          off[k][m] = splat2(0.f);
+        }
+        if (a.gamma)
+          IO::unpack(ld_shared_vec(static_cast<const uint4 *>(a.gamma) + k * NT + tid), fac[k]);
+        if (a.beta)
+          IO::unpack(ld_shared_vec(static_cast<const uint4 *>(a.beta) + k * NT + tid), off[k]);
+        if (a.scale) {
+          float2 sc[P], sh[P];
+          IO::unpack(ld_shared_vec(static_cast<const uint4 *>(a.scale) + koff + k * NT), sc);
+          IO::unpack(ld_shared_vec(static_cast<const uint4 *>(a.shift) + koff + k * NT), sh);
+#pragma unroll
+          for (int m = 0; m < P; ++m) {
+            sc[m] = add2(sc[m], splat2(1.f));
+            fac[k][m] = mul2(fac[k][m], sc[m]);
+            off[k][m] = fma2(off[k][m], sc[m], sh[m]);
+          }
+        }
+      }
+    }
+  };
+  auto load_row = [&](int q, float2 (&xq)[VPT][P]) -> float {
+    float2 acc = splat2(0.f);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      if (ok[k]) {
+        IO::unpack(*slot(cons, q, k), xq[k]);
+#pragma unroll
+        for (int m = 0; m < P; ++m) acc = add2(xq[k][m], acc);
+      }
+    }
+    return acc.x + acc.y;
+  };
+  auto spread = [&](const float2 (&xq)[VPT][P], float mu) -> float {
+    float2 acc = splat2(0.f);
+    const float2 neg = splat2(-mu);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      if (ok[k]) {
+#pragma unroll
+        for (int m = 0; m < P; ++m) {
+          const float2 d = add2(xq[k][m], neg);
+          acc = fma2(d, d, acc);
+        }
+      }
+    }
+    return acc.x + acc.y;
+  };
+  // (mean, rstd) of the row whose warp pairs are parked in red[buf][q]
+  auto combine = [&](int q) -> float2 {
+    const float2 *r = red + (buf * R + q) * NW;
+    float mean = 0.f, m2 = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) mean = fmaf(warp_elems(w) * inv_D, r[w].x, mean);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float d = r[w].x - mean;
+      m2 += fmaf(warp_elems(w) * d, d, r[w].y);
+    }
+    return make_float2(mean, rsqrtf(fmaf(m2, inv_D, a.eps)));
+  };
+  auto store_row = [&](int j, const float2 (&xq)[VPT][P], float2 st) {
+    const int64_t row = ro.row(j);
+    const float2 inv2 = splat2(st.y), neg = splat2(-st.x);
+    uint4 *yrow = reinterpret_cast<uint4 *>(yc + row * row_bytes) + tid;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      if (ok[k]) {
+        float2 o[P];
+#pragma unroll
+        for (int m = 0; m < P; ++m)
+          o[m] = fma2(add2(xq[k][m], neg), mul2(fac[k][m], inv2), off[k][m]);
+        st_stream16(yrow + k * NT, IO::pack(o));
+      }
+    }
+    if (a.mean && tid == 0) {
+      a.mean[row] = st.x;
+      a.rstd[row] = st.y;
+    }
+  };
+
+  for (int it = 0; it < iters; ++it) {
+    issue(it + S - 1, cons == 0 ? S - 1 : cons - 1);
+    if (ro.run_start(it * R)) cur.init(ro.row(it * R), a.L);
+    const int nrows = count - it * R < R ? count - it * R : R;
+    bool same = true;  // every row of this iteration uses the cached vectors
+    {
+      TokenCursor c = cur;
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        if (q < nrows) same &= (2 * c.b + (c.r >= a.n_video ? 1 : 0)) == key;
+        c.next(a.L);
+      }
+    }
+    cp_async_wait<S - 1>();
+
+    if (same) {
+      float2 xp[R][VPT][P];
+      float mu[R], m2[R];
+#pragma unroll
+      for (int q = 0; q < R; ++q) mu[q] = q < nrows ? load_row(q, xp[q]) : 0.f;
+#pragma unroll
+      for (int q = 0; q < R; ++q) mu[q] = warp_sum(mu[q]) * inv_nw;
+#pragma unroll
+      for (int q = 0; q < R; ++q) m2[q] = q < nrows ? spread(xp[q], mu[q]) : 0.f;
+#pragma unroll
+      for (int q = 0; q < R; ++q) m2[q] = warp_sum(m2[q]);
+      if (NW > 1) {
+        if (lane == 0) {
+#pragma unroll
+          for (int q = 0; q < R; ++q) red[(buf * R + q) * NW + warp] = make_float2(mu[q], m2[q]);
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int q = 0; q < R; ++q)
+        if (q < nrows) {
+          const float2 st = NW > 1 ? combine(q)
+                                   : make_float2(mu[q], rsqrtf(fmaf(m2[q], inv_D, a.eps)));
+          store_row(it * R + q, xp[q], st);
+        }
+#pragma unroll
+      for (int q = 0; q < R; ++q)
+        if (q < nrows) cur.next(a.L);
+    } else {
+      // a modality or sample boundary: rebuild the vectors row by row
+#pragma unroll 1
+      for (int q = 0; q < nrows; ++q) {
+        const int nkey = 2 * cur.b + (cur.r >= a.n_video ? 1 : 0);
+        if (nkey != key) {
+          key = nkey;
+          load_vectors();
+        }
+        float2 xq[VPT][P];
+        const float mu = warp_sum(load_row(q, xq)) * inv_nw;
+        const float m2 = warp_sum(spread(xq, mu));
+        float2 st;
+        if (NW > 1) {
+          if (lane == 0) red[(buf * R + q) * NW + warp] = make_float2(mu, m2);
+          __syncthreads();
+          st = combine(q);
+        } else {
+          st = make_float2(mu, rsqrtf(fmaf(m2, inv_D, a.eps)));
+        }
+        store_row(it * R + q, xq, st);
+        cur.next(a.L);
+      }
+    }
+    buf ^= 1;
+    cons = (cons + 1 == S) ? 0 : cons + 1;
+  }
+  cp_async_wait<0>();
+}
+
+template <int VPT>
+constexpr int kLnRows = VPT <= 5 ? 2 : 1;
+
+// chunk of consecutive rows per CTA turn, as RMS-AdaLN's
+constexpr int kLnChunk = 8;
+
+template <typename T, int NT, int VPT>
+cudaError_t launch_t(const LnArgs &a, cudaStream_t stream) {
+  constexpr int R = kLnRows<VPT>, S = 2;
+  auto *kern = &layer_norm_kernel<T, NT, VPT, R, S, kLnChunk>;
+  const void *fn = reinterpret_cast<const void *>(kern);
+  const size_t smem = 2 * R * (NT / 32) * 8 + static_cast<size_t>(S) * R * VPT * NT * 16;
+  const int per_sm = resident_blocks(fn, NT, smem);
+  if (per_sm <= 0) return cudaErrorInvalidConfiguration;
+  int64_t grid = static_cast<int64_t>(per_sm) * device_sms();
+  if (grid > a.rows) grid = a.rows;
+  kern<<<static_cast<unsigned>(grid), NT, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t dispatch(const LnArgs &a, int threads, int vpt, cudaStream_t stream) {
+#define SOL_CASE(NT, V) \
+  if (threads == NT && vpt == V) return launch_t<T, NT, V>(a, stream);
+  SOL_SPLITS(SOL_CASE)
+#undef SOL_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_layer_norm(const LnArgs &a, int dtype, cudaStream_t stream) {
+  int threads = 0, vpt = 0;
+  if (!pick_split(a.nvec, &threads, &vpt)) return cudaErrorInvalidValue;
+  return dtype == 0 ? dispatch<float>(a, threads, vpt, stream)
+                    : dispatch<__nv_bfloat16>(a, threads, vpt, stream);
+}
+
+}  // namespace sol

@@ -11,12 +11,14 @@
 #include <tuple>
 
 #include "sol.h"
+#include "sol_check.h"
 #include "sol_launch.h"
 
 namespace sol {
-namespace {
 
+namespace {
 thread_local std::string g_last_error;
+}  // namespace
 
 sol_status fail(sol_status s, const char *fmt, ...) {
   char buf[512];
@@ -37,41 +39,7 @@ sol_status cuda_fail(cudaError_t e, const char *what) {
   return fail(SOL_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int esize_of(sol_dtype dt) { return dt == SOL_F32 ? 4 : 2; }
-
-// Byte range [begin, end) touched by `rows` rows of `width` bytes, `ld`
-// bytes apart, starting at p.
-struct Span {
-  uintptr_t begin, end;
-};
-Span span_of(const void *p, int64_t rows, int64_t ld, int64_t width) {
-  uintptr_t b = reinterpret_cast<uintptr_t>(p);
-  return Span{b, b + static_cast<uintptr_t>((rows - 1) * ld + width)};
-}
-bool spans_overlap(Span a, Span b) { return a.begin < b.end && b.begin < a.end; }
-
-// True if the strided blocks A (base a, width wa) and B (base b, width wb),
-// both `rows` rows with the same row pitch `ld`, share no byte.  With equal
-// pitches, B's columns sit at offset c = (b - a) mod ld inside A's rows and
-// the blocks are disjoint when wa <= c <= ld - wb.
-bool strided_disjoint(const void *a, int64_t wa, const void *b, int64_t wb, int64_t rows,
-                      int64_t lda, int64_t ldb) {
-  if (!spans_overlap(span_of(a, rows, lda, wa), span_of(b, rows, ldb, wb))) return true;
-  if (lda != ldb) return false;
-  const int64_t off = static_cast<int64_t>(reinterpret_cast<intptr_t>(b) -
-                                           reinterpret_cast<intptr_t>(a));
-  int64_t c = off % lda;
-  if (c < 0) c += lda;
-  return wa <= c && c <= lda - wb;
-}
-
-// Identical or disjoint, for two contiguous [rows, width] tensors.
-bool same_or_disjoint(const void *a, const void *b, int64_t bytes) {
-  if (a == b) return true;
-  return !spans_overlap(span_of(a, 1, 0, bytes), span_of(b, 1, 0, bytes));
-}
+namespace {
 
 struct DevCache {
   std::mutex mu;
@@ -510,7 +478,7 @@ using namespace sol;
 
 extern "C" {
 
-int sol_version(void) { return (2 << 16) | 1; }
+int sol_version(void) { return (2 << 16) | 2; }
 
 const char *sol_status_string(sol_status s) {
   switch (s) {

@@ -14,20 +14,27 @@
 //
 // A thread owns one 16-byte vector of channels (NT threads span a tile of the
 // row's vectors, RG groups of them take different rows) and U rows at a time:
-// it issues the U rows' loads, computes the U vectors' words while they are
-// in flight and then writes.  The gate of the current (sample, modality)
-// stays in registers.
+// it issues the U rows' loads and computes the U vectors' words while they
+// arrive.  The gate of the current (sample, modality) stays in registers.
 //
-// Bound by HBM (3*D*esize bytes per row, forward and backward) with the
-// generator close behind: a Philox call is 20 wide multiplies and 20
-// three-input xors for four elements.
+// HBM traffic is 3*D*esize bytes per row, forward and backward, but the issue
+// slots are as scarce: a Philox call is 20 wide multiplies and 20 three-input
+// xors for four elements.  So the rest is kept small: a dropped element is a
+// predicated multiply-add that does not happen, the two calls of a bf16 vector
+// share the upper counter word and what depends on it alone, rows are 32-bit
+// indexes.
 #include "segment_sums.cuh"
 #include "sol_device.cuh"
 
 namespace sol {
 namespace {
 
-constexpr int kDropThreads = 256;  // bound on NT * RG
+// 128 threads with up to 128 registers, 4 rows each: 0.627 ms for the forward
+// pass at the 5 s clip, 0.653 ms for the backward (256 x 128 registers: 0.655 and
+// 0.683; 256 x 80: 0.677 and 0.733).
+constexpr int kDropThreads = 128;  // bound on NT * RG
+constexpr int kDropCtas = 4;       // CTAs per SM the registers are to leave room for
+constexpr int kDropRows = 4;       // rows per thread and pass
 
 // The ten round keys of a seed.
 struct PhiloxKey {
@@ -38,13 +45,15 @@ struct PhiloxKey {
     for (int r = 0; r < 10; ++r) {
       a[r] = x;
       b[r] = y;
+      // opaque: otherwise the keys are added up again in every call, 20 of its
+      // 60 instructions
+      asm volatile("" : "+r"(a[r]), "+r"(b[r]));
       x += 0x9E3779B9u;
       y += 0xBB67AE85u;
     }
   }
-  __device__ __forceinline__ uint4 words(uint64_t lo, uint64_t hi) const {
-    uint32_t c0 = static_cast<uint32_t>(lo), c1 = static_cast<uint32_t>(lo >> 32);
-    uint32_t c2 = static_cast<uint32_t>(hi), c3 = static_cast<uint32_t>(hi >> 32);
+  __device__ __forceinline__ uint4 words(uint32_t c0, uint32_t c1, uint32_t c2,
+                                         uint32_t c3) const {
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
       const uint64_t p0 = static_cast<uint64_t>(c0) * 0xD2511F53u;
@@ -59,49 +68,53 @@ struct PhiloxKey {
 };
 
 // 16-byte load not kept in L1: the tensors are read once.
-__device__ __forceinline__ uint4 ld_stream16(const uint4 *p) {
+__device__ __forceinline__ uint4 ld_stream16(const void *p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");
   return v;
 }
 
-// Bit i: element i of the vector at counter `ctr` is kept.
-template <int E>
-__device__ __forceinline__ uint32_t keep_bits(const PhiloxKey &key, uint64_t ctr, uint64_t hi,
-                                              uint32_t drop_max) {
-  uint32_t bits = 0;
-#pragma unroll
-  for (int i = 0; i < E / 4; ++i) {
-    const uint4 w = key.words(ctr + i, hi);
-    bits |= (w.x > drop_max ? 1u : 0u) << (4 * i);
-    bits |= (w.y > drop_max ? 2u : 0u) << (4 * i);
-    bits |= (w.z > drop_max ? 4u : 0u) << (4 * i);
-    bits |= (w.w > drop_max ? 8u : 0u) << (4 * i);
-  }
-  return bits;
+// acc += a * b where the word keeps the element.
+__device__ __forceinline__ void fma_kept(uint32_t word, uint32_t drop_max, float a, float b,
+                                         float &acc) {
+  asm("{\n\t.reg .pred p;\n\tsetp.gt.u32 p, %1, %2;\n\t@p fma.rn.f32 %0, %3, %4, %0;\n\t}"
+      : "+f"(acc)
+      : "r"(word), "r"(drop_max), "f"(a), "f"(b));
 }
-template <int P>
-__device__ __forceinline__ void drop_pairs(float2 (&v)[P], uint32_t bits) {
-#pragma unroll
-  for (int m = 0; m < P; ++m) {
-    v[m].x = (bits >> (2 * m)) & 1u ? v[m].x : 0.f;
-    v[m].y = (bits >> (2 * m + 1)) & 1u ? v[m].y : 0.f;
-  }
+// acc += a * b where the word keeps the element; prod becomes 0 where not.
+__device__ __forceinline__ void fma_select_kept(uint32_t word, uint32_t drop_max, float a, float b,
+                                                float &acc, float &prod) {
+  asm("{\n\t.reg .pred p;\n\tsetp.gt.u32 p, %2, %3;\n\t@p fma.rn.f32 %0, %4, %5, %0;\n\t"
+      "selp.f32 %1, %1, 0f00000000, p;\n\t}"
+      : "+f"(acc), "+f"(prod)
+      : "r"(word), "r"(drop_max), "f"(a), "f"(b));
 }
 
-template <typename T, bool DROP, bool RES, bool GATE, int U>
-__global__ void __launch_bounds__(kDropThreads) dropout_residual_kernel(const DropArgs a,
-                                                                        int tiles) {
+// The words of a vector of E elements; `ctr` is the counter of its first
+// element, a multiple of E / 4, so adding 1 for the second call carries nowhere.
+template <int E>
+__device__ __forceinline__ void vector_words(const PhiloxKey &key, uint64_t ctr, uint64_t hi,
+                                             uint4 (&w)[E / 4]) {
+  const uint32_t c0 = static_cast<uint32_t>(ctr), c1 = static_cast<uint32_t>(ctr >> 32);
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i)
+    w[i] = key.words(c0 + i, c1, static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32));
+}
+
+template <typename T, bool DROP, bool RES, bool GATE>
+__global__ void __launch_bounds__(kDropThreads, kDropCtas)
+    dropout_residual_kernel(const DropArgs a, int tiles) {
   using IO = Io<T>;
-  constexpr int P = IO::E / 2;
-  const int NT = blockDim.x, RG = blockDim.y, ty = threadIdx.y;
+  constexpr int E = IO::E, P = E / 2, U = kDropRows;
+  const int NT = blockDim.x, RG = blockDim.y;
   const int col = static_cast<int>(blockIdx.x % tiles) * NT + threadIdx.x;
-  if (col >= a.nvec) return;
-  const uint4 *branch = static_cast<const uint4 *>(a.branch) + col;
-  const uint4 *h = static_cast<const uint4 *>(a.h) + col;
-  uint4 *out = static_cast<uint4 *>(a.out) + col;
+  const int64_t row_bytes = static_cast<int64_t>(a.nvec) * 16, step = RG * row_bytes;
+  const unsigned char *branch = static_cast<const unsigned char *>(a.branch) + col * 16;
+  const unsigned char *h = static_cast<const unsigned char *>(a.h) + col * 16;
+  unsigned char *out = static_cast<unsigned char *>(a.out) + col * 16;
 
   PhiloxKey pk;
   uint64_t hi = 0;
@@ -109,68 +122,87 @@ __global__ void __launch_bounds__(kDropThreads) dropout_residual_kernel(const Dr
     pk.init(__ldg(reinterpret_cast<const unsigned long long *>(a.rng)));
     hi = __ldg(reinterpret_cast<const unsigned long long *>(a.rng) + 1) + a.site;
   }
-  float2 gt[P];  // gate * 1 / (1 - p) of `key`
+  if (col >= a.nvec) return;
+  float2 gt[P];  // gate * 1 / (1 - p) of the current (sample, modality)
 #pragma unroll
   for (int m = 0; m < P; ++m) gt[m] = splat2(a.keep_scale);
-  int key = -1;
+  int key_end = 0;  // first row past the ones `gt` is for
 
-  const int rows = static_cast<int>(a.seg.rows), L = a.seg.L;
-  const int step = RG * U;
-  // rows in blocks of `step` consecutive ones dealt round-robin over the CTAs
-  // of a tile, so the grid works through one window of the tensors
-  const int64_t stride = static_cast<int64_t>(gridDim.x / tiles) * step;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x / tiles) * step; r0 < rows; r0 += stride) {
-    const int first = static_cast<int>(r0) + ty;
+  // rows in blocks of RG * U consecutive ones dealt round-robin over the CTAs of
+  // a tile, so the grid works through one window of the tensors
+  const int rows = static_cast<int>(a.seg.rows), block = RG * U;
+  const int64_t stride = static_cast<int64_t>(gridDim.x / tiles) * block;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x / tiles) * block; r0 < rows; r0 += stride) {
+    // rows of this thread in the block: `first`, RG apart
+    const int64_t first64 = r0 + threadIdx.y;
+    const int first = static_cast<int>(first64);
+    const int n = first64 < rows ? (rows - 1 - first) / RG + 1 : 0;
+    const int64_t off = first64 * row_bytes;
+    const uint64_t ctr = (static_cast<uint64_t>(first64) * a.nvec + col) * (E / 4);
+    const uint32_t ctr_step = static_cast<uint32_t>(RG) * a.nvec * (E / 4);
     uint4 vb[U], vh[U];
+    auto load = [&](int u) {
+      vb[u] = ld_stream16(branch + off + u * step);
+      if constexpr (RES) vh[u] = ld_stream16(h + off + u * step);
+    };
+    auto finish = [&](int u) {
+      float2 x[P], o[P];
+      IO::unpack(vb[u], x);
+      if constexpr (RES) IO::unpack(vh[u], o);
+      if constexpr (DROP) {
+        uint4 w[E / 4];
+        vector_words<E>(pk, ctr + u * ctr_step, hi, w);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = static_cast<int64_t>(first) + u * RG;
-      if (row < rows) {
-        vb[u] = ld_stream16(branch + row * a.nvec);
-        if constexpr (RES) vh[u] = ld_stream16(h + row * a.nvec);
-      }
-    }
-    int b = 0, r = 0;
-    if constexpr (GATE) {
-      b = first / L;
-      r = first - b * L;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = static_cast<int64_t>(first) + u * RG;
-      if (row < rows) {
-        if constexpr (GATE) {
-          const int nkey = 2 * b + (r >= a.seg.n_video ? 1 : 0);
-          if (nkey != key) {
-            key = nkey;
-            IO::unpack(ld_shared_vec(static_cast<const uint4 *>(a.gate) +
-                                     static_cast<int64_t>(key) * a.nvec + col),
-                       gt);
-#pragma unroll
-            for (int m = 0; m < P; ++m) gt[m] = mul2(gt[m], splat2(a.keep_scale));
+        for (int i = 0; i < E / 4; ++i) {
+          float2 &x0 = x[2 * i], &x1 = x[2 * i + 1];
+          if constexpr (RES) {
+            float2 &o0 = o[2 * i], &o1 = o[2 * i + 1];
+            fma_kept(w[i].x, a.drop_max, gt[2 * i].x, x0.x, o0.x);
+            fma_kept(w[i].y, a.drop_max, gt[2 * i].y, x0.y, o0.y);
+            fma_kept(w[i].z, a.drop_max, gt[2 * i + 1].x, x1.x, o1.x);
+            fma_kept(w[i].w, a.drop_max, gt[2 * i + 1].y, x1.y, o1.y);
+          } else {
+            x0 = mul2(gt[2 * i], x0);
+            x1 = mul2(gt[2 * i + 1], x1);
+            o[2 * i].x = w[i].x > a.drop_max ? x0.x : 0.f;
+            o[2 * i].y = w[i].y > a.drop_max ? x0.y : 0.f;
+            o[2 * i + 1].x = w[i].z > a.drop_max ? x1.x : 0.f;
+            o[2 * i + 1].y = w[i].w > a.drop_max ? x1.y : 0.f;
           }
         }
-        float2 x[P], o[P];
-        IO::unpack(vb[u], x);
-        if constexpr (DROP) {
-          const uint64_t ctr = (static_cast<uint64_t>(row) * a.nvec + col) * (IO::E / 4);
-          drop_pairs(x, keep_bits<IO::E>(pk, ctr, hi, a.drop_max));
-        }
-        if constexpr (RES) {
-          IO::unpack(vh[u], o);
+      } else {
 #pragma unroll
-          for (int m = 0; m < P; ++m) o[m] = fma2(gt[m], x[m], o[m]);
-        } else {
-#pragma unroll
-          for (int m = 0; m < P; ++m) o[m] = mul2(gt[m], x[m]);
-        }
-        st_stream16(out + row * a.nvec, IO::pack(o));
+        for (int m = 0; m < P; ++m) o[m] = RES ? fma2(gt[m], x[m], o[m]) : mul2(gt[m], x[m]);
       }
-      if constexpr (GATE) {
-        r += RG;
-        while (r >= L) {
-          r -= L;
-          ++b;
+      st_stream16(out + off + u * step, IO::pack(o));
+    };
+    if (n >= U && (!GATE || first + (U - 1) * RG < key_end)) {
+      // a whole block under the present gate
+#pragma unroll
+      for (int u = 0; u < U; ++u) load(u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) finish(u);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < n) load(u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u < n) {
+          if constexpr (GATE) {
+            if (first + u * RG >= key_end) {
+              const int key = key_of(a.seg, first + u * RG);
+              int64_t begin, end;
+              key_rows(a.seg, key, &begin, &end);
+              key_end = static_cast<int>(end);
+              IO::unpack(ld_shared_vec(static_cast<const uint4 *>(a.gate) +
+                                       static_cast<int64_t>(key) * a.nvec + col),
+                         gt);
+#pragma unroll
+              for (int m = 0; m < P; ++m) gt[m] = mul2(gt[m], splat2(a.keep_scale));
+            }
+          }
+          finish(u);
         }
       }
     }
@@ -179,20 +211,21 @@ __global__ void __launch_bounds__(kDropThreads) dropout_residual_kernel(const Dr
 
 // blockIdx.x = tile + tiles * share; the rows of a share are cut into runs of
 // one (sample, modality), whose sums go to slot share + key.
-template <typename T, bool DROP, int U>
-__global__ void __launch_bounds__(kDropThreads) dropout_backward_kernel(const DropArgs a,
-                                                                        int tiles) {
+template <typename T, bool DROP>
+__global__ void __launch_bounds__(kDropThreads, kDropCtas)
+    dropout_backward_kernel(const DropArgs a, int tiles) {
   using IO = Io<T>;
-  constexpr int P = IO::E / 2;
+  constexpr int E = IO::E, P = E / 2, U = kDropRows;
   __shared__ float2 park[P * kDropThreads];
   const int NT = blockDim.x, RG = blockDim.y, ty = threadIdx.y;
   const int tid = ty * NT + threadIdx.x;
   const int share = static_cast<int>(blockIdx.x / tiles);
   const int col = static_cast<int>(blockIdx.x % tiles) * NT + threadIdx.x;
   const bool ok = col < a.nvec;
-  const uint4 *branch = static_cast<const uint4 *>(a.branch) + col;
-  const uint4 *dout = static_cast<const uint4 *>(a.dout) + col;
-  uint4 *out = static_cast<uint4 *>(a.out) + col;
+  const int64_t row_bytes = static_cast<int64_t>(a.nvec) * 16, step = RG * row_bytes;
+  const unsigned char *branch = static_cast<const unsigned char *>(a.branch) + col * 16;
+  const unsigned char *dout = static_cast<const unsigned char *>(a.dout) + col * 16;
+  unsigned char *out = static_cast<unsigned char *>(a.out) + col * 16;
 
   PhiloxKey pk;
   uint64_t hi = 0;
@@ -218,38 +251,52 @@ __global__ void __launch_bounds__(kDropThreads) dropout_backward_kernel(const Dr
                  gt);
 #pragma unroll
       for (int m = 0; m < P; ++m) gt[m] = mul2(gt[m], splat2(a.keep_scale));
-      for (int64_t r0 = row + ty; r0 < run_end; r0 += RG * U) {
-        uint4 vd[U], vb[U];
+      // rows of this thread in the run
+      const int64_t first = row + ty;
+      int n = first < run_end ? static_cast<int>((run_end - 1 - first) / RG) + 1 : 0;
+      int64_t off = first * row_bytes;
+      uint64_t ctr = (static_cast<uint64_t>(first) * a.nvec + col) * (E / 4);
+      const uint32_t ctr_step = static_cast<uint32_t>(RG) * a.nvec * (E / 4);
+      uint4 vd[U], vb[U];
+      auto load = [&](int u) {
+        vd[u] = ld_stream16(dout + off + u * step);
+        vb[u] = ld_stream16(branch + off + u * step);
+      };
+      auto finish = [&](int u) {
+        float2 d[P], x[P], o[P];
+        IO::unpack(vd[u], d);
+        IO::unpack(vb[u], x);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t r = r0 + u * RG;
-          if (r < run_end) {
-            vd[u] = ld_stream16(dout + r * a.nvec);
-            vb[u] = ld_stream16(branch + r * a.nvec);
+        for (int m = 0; m < P; ++m) o[m] = mul2(gt[m], d[m]);
+        if constexpr (DROP) {
+          uint4 w[E / 4];
+          vector_words<E>(pk, ctr + u * ctr_step, hi, w);
+#pragma unroll
+          for (int i = 0; i < E / 4; ++i) {
+            const int m = 2 * i;
+            fma_select_kept(w[i].x, a.drop_max, d[m].x, x[m].x, sum[m].x, o[m].x);
+            fma_select_kept(w[i].y, a.drop_max, d[m].y, x[m].y, sum[m].y, o[m].y);
+            fma_select_kept(w[i].z, a.drop_max, d[m + 1].x, x[m + 1].x, sum[m + 1].x, o[m + 1].x);
+            fma_select_kept(w[i].w, a.drop_max, d[m + 1].y, x[m + 1].y, sum[m + 1].y, o[m + 1].y);
           }
-        }
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t r = r0 + u * RG;
-          if (r < run_end) {
-            float2 d[P], x[P];
-            IO::unpack(vd[u], d);
-            IO::unpack(vb[u], x);
-            if constexpr (DROP) {
-              const uint64_t ctr = (static_cast<uint64_t>(r) * a.nvec + col) * (IO::E / 4);
-              const uint32_t bits = keep_bits<IO::E>(pk, ctr, hi, a.drop_max);
-              drop_pairs(d, bits);
-              drop_pairs(x, bits);  // an infinite branch value adds nothing where dropped
-            }
-#pragma unroll
-            for (int m = 0; m < P; ++m) {
-              sum[m] = fma2(d[m], x[m], sum[m]);
-              d[m] = mul2(gt[m], d[m]);
-            }
-            st_stream16(out + r * a.nvec, IO::pack(d));
-          }
+          for (int m = 0; m < P; ++m) sum[m] = fma2(d[m], x[m], sum[m]);
         }
+        st_stream16(out + off + u * step, IO::pack(o));
+      };
+      for (; n >= U; n -= U, off += U * step, ctr += U * ctr_step) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) load(u);
+#pragma unroll
+        for (int u = 0; u < U; ++u) finish(u);
       }
+#pragma unroll
+      for (int u = 0; u < U - 1; ++u)
+        if (u < n) load(u);
+#pragma unroll
+      for (int u = 0; u < U - 1; ++u)
+        if (u < n) finish(u);
     }
     if (RG > 1) {
       if (ty > 0) {
@@ -294,15 +341,14 @@ void pick_tiles(int nvec, int *tiles, int *nt) {
 
 template <typename T, bool DROP, bool RES, bool GATE>
 cudaError_t launch_fwd(const DropArgs &a, cudaStream_t stream) {
-  constexpr int U = 4;
   int tiles = 1, nt = 32;
   pick_tiles(a.nvec, &tiles, &nt);
   const int rg = kDropThreads / nt;
-  auto *kern = &dropout_residual_kernel<T, DROP, RES, GATE, U>;
+  auto *kern = &dropout_residual_kernel<T, DROP, RES, GATE>;
   const int per_sm = resident_blocks(reinterpret_cast<const void *>(kern), nt * rg, 0);
   if (per_sm <= 0) return cudaErrorInvalidConfiguration;
   int64_t shares = static_cast<int64_t>(per_sm) * device_sms() / tiles;
-  const int64_t most = (a.seg.rows + rg * U - 1) / (rg * U);
+  const int64_t most = (a.seg.rows + rg * kDropRows - 1) / (rg * kDropRows);
   if (shares > most) shares = most;
   if (shares < 1) shares = 1;
   kern<<<static_cast<unsigned>(shares * tiles), dim3(nt, rg), 0, stream>>>(a, tiles);
@@ -311,20 +357,19 @@ cudaError_t launch_fwd(const DropArgs &a, cudaStream_t stream) {
 
 template <typename T, bool DROP>
 cudaError_t launch_bwd(DropArgs &a, cudaStream_t stream) {
-  constexpr int U = 4;
   int tiles = 1, nt = 32;
   pick_tiles(a.nvec, &tiles, &nt);
   const int rg = kDropThreads / nt;
-  auto *kern = &dropout_backward_kernel<T, DROP, U>;
+  auto *kern = &dropout_backward_kernel<T, DROP>;
   const int per_sm = resident_blocks(reinterpret_cast<const void *>(kern), nt * rg, 0);
   if (per_sm <= 0) return cudaErrorInvalidConfiguration;
   int64_t shares = static_cast<int64_t>(per_sm) * device_sms() / tiles;
-  const int64_t most = (a.seg.rows + rg * U - 1) / (rg * U);
+  const int64_t most = (a.seg.rows + rg * kDropRows - 1) / (rg * kDropRows);
   if (shares > most) shares = most;
   if (shares > kMaxSumCtas) shares = kMaxSumCtas;
   if (shares < 1) shares = 1;
   a.seg.ctas = static_cast<int>(shares);
-  kern<<<static_cast<unsigned>(shares * tiles), dim3(nt, rg), 0, stream>>>(a, tiles);
+  kern<<<static_cast<unsigned>(a.seg.ctas * tiles), dim3(nt, rg), 0, stream>>>(a, tiles);
   return cudaGetLastError();
 }
 

@@ -12,8 +12,8 @@
 //
 // Statistics in one barrier: each warp takes the mean of its own slice of the
 // row and the sum of squares about it, both from registers, and the warps'
-// (mean, M2) pairs are combined exactly,
-//   mean = sum n_w mean_w / D,  M2 = sum M2_w + n_w (mean_w - mean)^2,
+// (sum, M2) pairs are combined exactly,
+//   mean = sum sum_w / D,  M2 = sum M2_w + n_w (mean_w - mean)^2,
 // so a row whose mean is large against its spread loses no digits, as
 // mean(x^2) - mean^2 would.
 //
@@ -24,15 +24,33 @@
 namespace sol {
 namespace {
 
+// A staged vector, read again at each use: holding a row's unpacked channels
+// across the reductions took 252 registers at 128 x 5 and left 8 warps on an
+// SM (0.469 ms at the 5 s clip).
+__device__ __forceinline__ uint4 ld_staged(const uint4 *p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(smem_u32(p))
+               : "memory");
+  return v;
+}
+
+// Threads per SM that the registers are to leave room for (128 registers a
+// thread): 0.424 ms at the 5 s clip, against 0.449 ms without the bound (150
+// registers) and 0.78 ms at 96 registers, which spill.
+constexpr int kLnThreadsPerSm = 512;
+
 template <typename T, int NT, int VPT, int R, int S, int K>
-__global__ void __launch_bounds__(NT) layer_norm_kernel(const LnArgs a) {
+__global__ void __launch_bounds__(NT, kLnThreadsPerSm / NT < 16 ? kLnThreadsPerSm / NT : 16)
+    layer_norm_kernel(const LnArgs a) {
   static_assert(K % R == 0, "an iteration's rows must lie in one chunk");
   using IO = Io<T>;
   constexpr int P = IO::E / 2;
   constexpr int NW = NT / 32;
   extern __shared__ __align__(16) unsigned char smem[];
-  float2 *red = reinterpret_cast<float2 *>(smem);                   // [2][R][NW]: mean_w, M2_w
-  uint4 *ring = reinterpret_cast<uint4 *>(smem + 2 * R * NW * 8);  // [S][R][VPT][NT]
+  float4 *red = reinterpret_cast<float4 *>(smem);  // [2][R][NW]: sum_w, M2_w, mean_w, n_w
+  uint4 *ring = reinterpret_cast<uint4 *>(smem + 2 * R * NW * 16);  // [S][R][VPT][NT]
 
   const int tid = threadIdx.x;
   const int lane = tid & 31;
@@ -43,19 +61,14 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const LnArgs a) {
   bool ok[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) ok[k] = k * NT + tid < a.nvec;
-  // elements of a row that warp w holds
-  auto warp_elems = [&](int w) -> float {
-    int n = 0;
+  // elements of a row that this warp holds
+  float n_w = 0.f;
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      int m = a.nvec - k * NT - w * 32;
-      m = m < 0 ? 0 : (m > 32 ? 32 : m);
-      n += m;
-    }
-    return static_cast<float>(n * IO::E);
-  };
-  const float nw_mine = warp_elems(warp);
-  const float inv_nw = nw_mine > 0.f ? 1.f / nw_mine : 0.f;
+  for (int k = 0; k < VPT; ++k) {
+    const int m = a.nvec - k * NT - warp * 32;
+    n_w += static_cast<float>((m < 0 ? 0 : (m > 32 ? 32 : m)) * IO::E);
+  }
+  const float inv_nw = n_w > 0.f ? 1.f / n_w : 0.f;
 
   RowOrder<K, R> ro;
   ro.init(a.rows);
@@ -118,57 +131,66 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const LnArgs a) {
       }
     }
   };
-  auto load_row = [&](int q, float2 (&xq)[VPT][P]) -> float {
+  auto row_sum = [&](int q) -> float {
     float2 acc = splat2(0.f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       if (ok[k]) {
-        IO::unpack(*slot(cons, q, k), xq[k]);
+        float2 x[P];
+        IO::unpack(ld_staged(slot(cons, q, k)), x);
 #pragma unroll
-        for (int m = 0; m < P; ++m) acc = add2(xq[k][m], acc);
+        for (int m = 0; m < P; ++m) acc = add2(x[m], acc);
       }
     }
     return acc.x + acc.y;
   };
-  auto spread = [&](const float2 (&xq)[VPT][P], float mu) -> float {
+  auto spread = [&](int q, float mu) -> float {
     float2 acc = splat2(0.f);
     const float2 neg = splat2(-mu);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       if (ok[k]) {
+        float2 x[P];
+        IO::unpack(ld_staged(slot(cons, q, k)), x);
 #pragma unroll
         for (int m = 0; m < P; ++m) {
-          const float2 d = add2(xq[k][m], neg);
+          const float2 d = add2(x[m], neg);
           acc = fma2(d, d, acc);
         }
       }
     }
     return acc.x + acc.y;
   };
-  // (mean, rstd) of the row whose warp pairs are parked in red[buf][q]
+  // (mean, rstd) of the row whose warp sums are parked in red[buf][q]
   auto combine = [&](int q) -> float2 {
-    const float2 *r = red + (buf * R + q) * NW;
-    float mean = 0.f, m2 = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) mean = fmaf(warp_elems(w) * inv_D, r[w].x, mean);
+    const float4 *r = red + (buf * R + q) * NW;
+    float4 v[NW];
+    float sum = 0.f, m2 = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      const float d = r[w].x - mean;
-      m2 += fmaf(warp_elems(w) * d, d, r[w].y);
+      v[w] = r[w];
+      sum += v[w].x;
+    }
+    const float mean = sum * inv_D;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float d = v[w].z - mean;
+      m2 += fmaf(v[w].w * d, d, v[w].y);
     }
     return make_float2(mean, rsqrtf(fmaf(m2, inv_D, a.eps)));
   };
-  auto store_row = [&](int j, const float2 (&xq)[VPT][P], float2 st) {
+  auto store_row = [&](int q, int j, float2 st) {
     const int64_t row = ro.row(j);
     const float2 inv2 = splat2(st.y), neg = splat2(-st.x);
     uint4 *yrow = reinterpret_cast<uint4 *>(yc + row * row_bytes) + tid;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       if (ok[k]) {
-        float2 o[P];
+        float2 x[P], o[P];
+        IO::unpack(ld_staged(slot(cons, q, k)), x);
 #pragma unroll
         for (int m = 0; m < P; ++m)
-          o[m] = fma2(add2(xq[k][m], neg), mul2(fac[k][m], inv2), off[k][m]);
+          o[m] = fma2(add2(x[m], neg), mul2(fac[k][m], inv2), off[k][m]);
         st_stream16(yrow + k * NT, IO::pack(o));
       }
     }
@@ -194,20 +216,23 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const LnArgs a) {
     cp_async_wait<S - 1>();
 
     if (same) {
-      float2 xp[R][VPT][P];
-      float mu[R], m2[R];
+      float sum[R], mu[R], m2[R];
 #pragma unroll
-      for (int q = 0; q < R; ++q) mu[q] = q < nrows ? load_row(q, xp[q]) : 0.f;
+      for (int q = 0; q < R; ++q) sum[q] = q < nrows ? row_sum(q) : 0.f;
 #pragma unroll
-      for (int q = 0; q < R; ++q) mu[q] = warp_sum(mu[q]) * inv_nw;
+      for (int q = 0; q < R; ++q) {
+        sum[q] = warp_sum(sum[q]);
+        mu[q] = sum[q] * inv_nw;
+      }
 #pragma unroll
-      for (int q = 0; q < R; ++q) m2[q] = q < nrows ? spread(xp[q], mu[q]) : 0.f;
+      for (int q = 0; q < R; ++q) m2[q] = q < nrows ? spread(q, mu[q]) : 0.f;
 #pragma unroll
       for (int q = 0; q < R; ++q) m2[q] = warp_sum(m2[q]);
       if (NW > 1) {
         if (lane == 0) {
 #pragma unroll
-          for (int q = 0; q < R; ++q) red[(buf * R + q) * NW + warp] = make_float2(mu[q], m2[q]);
+          for (int q = 0; q < R; ++q)
+            red[(buf * R + q) * NW + warp] = make_float4(sum[q], m2[q], mu[q], n_w);
         }
         __syncthreads();
       }
@@ -216,7 +241,7 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const LnArgs a) {
         if (q < nrows) {
           const float2 st = NW > 1 ? combine(q)
                                    : make_float2(mu[q], rsqrtf(fmaf(m2[q], inv_D, a.eps)));
-          store_row(it * R + q, xp[q], st);
+          store_row(q, it * R + q, st);
         }
 #pragma unroll
       for (int q = 0; q < R; ++q)
@@ -230,18 +255,18 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const LnArgs a) {
           key = nkey;
           load_vectors();
         }
-        float2 xq[VPT][P];
-        const float mu = warp_sum(load_row(q, xq)) * inv_nw;
-        const float m2 = warp_sum(spread(xq, mu));
+        const float sum = warp_sum(row_sum(q));
+        const float mu = sum * inv_nw;
+        const float m2 = warp_sum(spread(q, mu));
         float2 st;
         if (NW > 1) {
-          if (lane == 0) red[(buf * R + q) * NW + warp] = make_float2(mu, m2);
+          if (lane == 0) red[(buf * R + q) * NW + warp] = make_float4(sum, m2, mu, n_w);
           __syncthreads();
           st = combine(q);
         } else {
           st = make_float2(mu, rsqrtf(fmaf(m2, inv_D, a.eps)));
         }
-        store_row(it * R + q, xq, st);
+        store_row(q, it * R + q, st);
         cur.next(a.L);
       }
     }
@@ -262,7 +287,7 @@ cudaError_t launch_t(const LnArgs &a, cudaStream_t stream) {
   constexpr int R = kLnRows<VPT>, S = 2;
   auto *kern = &layer_norm_kernel<T, NT, VPT, R, S, kLnChunk>;
   const void *fn = reinterpret_cast<const void *>(kern);
-  const size_t smem = 2 * R * (NT / 32) * 8 + static_cast<size_t>(S) * R * VPT * NT * 16;
+  const size_t smem = 2 * R * (NT / 32) * 16 + static_cast<size_t>(S) * R * VPT * NT * 16;
   const int per_sm = resident_blocks(fn, NT, smem);
   if (per_sm <= 0) return cudaErrorInvalidConfiguration;
   int64_t grid = static_cast<int64_t>(per_sm) * device_sms();

@@ -34,13 +34,30 @@ constexpr int kNormThreads = VPT <= 2 ? 320 : 512;
 template <int VPT>
 constexpr int kNormCtas = VPT <= 2 ? 2 : 1;
 
-// S ring stages of R rows per group.
+// Sums of up to four values over the warp with six shuffles: after it lane 8i
+// holds the sum of value i.  Each step sends the values that the partner keeps.
+__device__ __forceinline__ float warp_sum4(float a, float b, float c, float d, int lane) {
+  const bool hi = lane & 16, mid = lane & 8;
+  float u = hi ? c : a, v = hi ? d : b;
+  u += __shfl_xor_sync(0xffffffffu, hi ? a : c, 16);
+  v += __shfl_xor_sync(0xffffffffu, hi ? b : d, 16);
+  float w = mid ? v : u;
+  w += __shfl_xor_sync(0xffffffffu, mid ? u : v, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+  return w;
+}
+
+// S ring stages of R (1 or 2) rows per group.  Each warp has a block of the
+// ring to itself, its slots 512 bytes (a vector per lane) apart: every slot is
+// a constant offset whatever the CTA's shape.
 template <typename T, int VPT, bool RMS, bool DRES, int R, int S>
 __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
     norm_backward_kernel(const NormBwdArgs a) {
   using IO = Io<T>;
   constexpr int P = IO::E / 2;
   constexpr int NIN = DRES ? 3 : 2;  // staged per row: x, dy, [dres]
+  constexpr int STAGE = R * NIN * VPT;
   extern __shared__ __align__(16) unsigned char smem[];
 
   const int NT = blockDim.x, RG = blockDim.y;
@@ -49,9 +66,9 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
   const int NW = NT >> 5;
   const int lane = tx & 31, warp = tx >> 5;
   const int threads = NT * RG;
-  float2 *red = reinterpret_cast<float2 *>(smem);  // [2][RG][NW][R]
-  uint4 *ring = reinterpret_cast<uint4 *>(smem + ((2 * RG * NW * R * 8 + 15) & ~15));
-  // ring: [S][R][NIN][VPT][threads]
+  float4 *red = reinterpret_cast<float4 *>(smem);  // [2][RG][NW]: two sums of two rows
+  uint4 *ring = reinterpret_cast<uint4 *>(red + 2 * RG * NW);  // [warp][S * STAGE][32]
+  uint4 *mine = ring + (tid >> 5) * (S * STAGE * 32) + lane;
 
   const int64_t row_bytes = static_cast<int64_t>(a.nvec) * 16;
   const unsigned char *src[3] = {static_cast<const unsigned char *>(a.x),
@@ -60,11 +77,12 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
   unsigned char *dxc = static_cast<unsigned char *>(a.dx);
   const float inv_D = 1.f / static_cast<float>(a.D);
 
-  bool ok[VPT];
-#pragma unroll
-  for (int k = 0; k < VPT; ++k) ok[k] = k * NT + tx < a.nvec;
+  // Only the last vector of a thread can lie past the row: the launcher's NT
+  // has (VPT - 1) * NT <= nvec.
+  const bool last = (VPT - 1) * NT + tx < a.nvec;
+  auto ok = [&](int k) { return k < VPT - 1 || last; };
   auto slot = [&](int s, int q, int in, int k) -> uint4 * {
-    return &ring[(((s * R + q) * NIN + in) * VPT + k) * threads + tid];
+    return mine + (s * STAGE + (q * NIN + in) * VPT + k) * 32;
   };
 
   int buf = 0;  // which half of `red`
@@ -88,7 +106,7 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
         s1[k][m] = splat2(0.f);
         s0[k][m] = splat2(0.f);
       }
-      if (ok[k]) {
+      if (ok(k)) {
         if (a.gamma)
           IO::unpack(ld_shared_vec(static_cast<const uint4 *>(a.gamma) + k * NT + tx), W[k]);
         if (a.scale) {
@@ -112,7 +130,7 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
           for (int in = 0; in < NIN; ++in)
 #pragma unroll
             for (int k = 0; k < VPT; ++k)
-              if (ok[k]) cp_async16(slot(s, q, in, k), src[in] + off + k * NT * 16);
+              if (ok(k)) cp_async16(slot(s, q, in, k), src[in] + off + k * NT * 16);
         }
       }
       cp_async_commit();
@@ -138,16 +156,16 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
       load_stats(it + 1, st_next);
       cp_async_wait<S - 1>();
 
-      // the row's two sums: layer norm (g, g * (x - mean)), RMS (x^2, g * x)
+      // the row's two sums: layer norm (g, g * x^), RMS (x^2, g * x)
       float2 sum[R];
 #pragma unroll
       for (int q = 0; q < R; ++q) {
         float2 u = splat2(0.f), v = splat2(0.f);
         if (it * step + ty * R + q < count) {
-          const float2 neg = splat2(-st[q].x);
+          const float2 r2 = splat2(st[q].y), off = splat2(-st[q].x * st[q].y);
 #pragma unroll
           for (int k = 0; k < VPT; ++k) {
-            if (ok[k]) {
+            if (ok(k)) {
               float2 x[P], d[P];
               IO::unpack(*slot(cons, q, 0, k), x);
               IO::unpack(*slot(cons, q, 1, k), d);
@@ -159,7 +177,7 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
                   v = fma2(g, x[m], v);
                 } else {
                   u = add2(g, u);
-                  v = fma2(g, add2(x[m], neg), v);
+                  v = fma2(g, fma2(x[m], r2, off), v);
                 }
               }
             }
@@ -167,54 +185,60 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
         }
         sum[q] = make_float2(u.x + u.y, v.x + v.y);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-          sum[q].x += __shfl_xor_sync(0xffffffffu, sum[q].x, o);
-          sum[q].y += __shfl_xor_sync(0xffffffffu, sum[q].y, o);
-        }
-      }
+      const float part = warp_sum4(sum[0].x, sum[0].y, sum[R - 1].x, sum[R - 1].y, lane);
       if (NW > 1) {
-        float2 *r = red + (buf * RG + ty) * NW * R;
-        if (lane == 0) {
-#pragma unroll
-          for (int q = 0; q < R; ++q) r[warp * R + q] = sum[q];
-        }
+        float4 *r = red + (buf * RG + ty) * NW;
+        if ((lane & 7) == 0) reinterpret_cast<float *>(r + warp)[lane >> 3] = part;
         __syncthreads();
-#pragma unroll
-        for (int q = 0; q < R; ++q) sum[q] = splat2(0.f);
-        for (int w = 0; w < NW; ++w)
-#pragma unroll
-          for (int q = 0; q < R; ++q) sum[q] = add2(sum[q], r[w * R + q]);
+        float2 t0 = splat2(0.f), t1 = splat2(0.f);
+#pragma unroll 4
+        for (int w = 0; w < NW; ++w) {
+          const float4 v = r[w];
+          t0 = add2(t0, make_float2(v.x, v.y));
+          t1 = add2(t1, make_float2(v.z, v.w));
+        }
+        sum[0] = t0;
+        if constexpr (R == 2) sum[1] = t1;
         buf ^= 1;
+      } else {
+        sum[0].x = __shfl_sync(0xffffffffu, part, 0);
+        sum[0].y = __shfl_sync(0xffffffffu, part, 8);
+        if constexpr (R == 2) {
+          sum[1].x = __shfl_sync(0xffffffffu, part, 16);
+          sum[1].y = __shfl_sync(0xffffffffu, part, 24);
+        }
       }
 
 #pragma unroll
       for (int q = 0; q < R; ++q) {
         const int j = it * step + ty * R + q;
         if (j < count) {
-          // dx = rstd * g + a1 * (x - mean) + a0
+          // dx = rstd * g + a1 * x^ + a0
           const float rstd = RMS ? rsqrtf(fmaf(sum[q].x, inv_D, a.eps)) : st[q].y;
-          const float a1 = -rstd * rstd * rstd * sum[q].y * inv_D;
-          const float a0 = RMS ? 0.f : -rstd * sum[q].x * inv_D;
-          const float2 neg = splat2(-st[q].x), r2 = splat2(rstd), a12 = splat2(a1),
-                       a02 = splat2(a0);
+          const float m2 = (RMS ? rstd * sum[q].y : sum[q].y) * inv_D;
+          const float2 a1 = splat2(-rstd * m2), a0 = splat2(-rstd * sum[q].x * inv_D);
+          const float2 r2 = splat2(rstd), off = splat2(-st[q].x * rstd);
           uint4 *out = reinterpret_cast<uint4 *>(dxc + (row + j) * row_bytes) + tx;
 #pragma unroll
           for (int k = 0; k < VPT; ++k) {
-            if (ok[k]) {
+            if (ok(k)) {
               float2 x[P], d[P], o[P];
               IO::unpack(*slot(cons, q, 0, k), x);
               IO::unpack(*slot(cons, q, 1, k), d);
               if constexpr (DRES) IO::unpack(*slot(cons, q, 2, k), o);
 #pragma unroll
               for (int m = 0; m < P; ++m) {
-                if constexpr (!RMS) x[m] = add2(x[m], neg);
-                s1[k][m] = fma2(mul2(x[m], r2), d[m], s1[k][m]);
+                const float2 xh = RMS ? mul2(x[m], r2) : fma2(x[m], r2, off);
+                s1[k][m] = fma2(xh, d[m], s1[k][m]);
                 s0[k][m] = add2(s0[k][m], d[m]);
-                const float2 base = DRES ? add2(o[m], a02) : a02;
-                o[m] = fma2(mul2(d[m], W[k][m]), r2, fma2(x[m], a12, base));
+                const float2 g = mul2(d[m], W[k][m]);
+                if constexpr (DRES) {
+                  o[m] = fma2(xh, a1, o[m]);
+                  if constexpr (!RMS) o[m] = add2(o[m], a0);
+                } else {
+                  o[m] = RMS ? mul2(xh, a1) : fma2(xh, a1, a0);
+                }
+                o[m] = fma2(g, r2, o[m]);
               }
               st_stream16(out + k * NT, IO::pack(o));
             }
@@ -257,7 +281,7 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
       if (ty == 0) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-          if (ok[k]) {
+          if (ok(k)) {
             float2 *p1 = reinterpret_cast<float2 *>(dst) + (k * NT + tx) * P;
             float2 *p0 = reinterpret_cast<float2 *>(dst + a.D) + (k * NT + tx) * P;
 #pragma unroll
@@ -279,7 +303,7 @@ cudaError_t launch_t(NormBwdArgs &a, cudaStream_t stream) {
   const int NT = ((a.nvec + VPT - 1) / VPT + 31) / 32 * 32;
   const int RG = NT >= 256 ? 1 : 256 / NT;
   auto *kern = &norm_backward_kernel<T, VPT, RMS, DRES, R, S>;
-  const size_t smem = ((2 * RG * (NT / 32) * R * 8 + 15) & ~15) +
+  const size_t smem = 2 * RG * (NT / 32) * 16 +
                       static_cast<size_t>(S) * R * (DRES ? 3 : 2) * VPT * NT * RG * 16;
   const int per_sm =
       resident_blocks(reinterpret_cast<const void *>(kern), NT * RG, smem);

@@ -8,18 +8,26 @@
 // where R(pos) turns pair i of the first rot_dim channels by the angle
 // pos[axis_i] * freq_i and leaves the rest as they are.
 //
-// A CTA takes tiles of `tile_rows` token rows.  Its threads first compute the
-// tile's angles, once for all q and k heads: the product in fp64, reduced to
-// [-pi, pi] by a two-part 2 pi, then sin and cos of the fp32 rest, corrected
-// to first order by what that rounding dropped.  cos and sin go to shared
-// memory (two buffers, so one barrier per tile).  Then G consecutive lanes own
-// one head vector at a time (16 bytes per lane; G is the next power of two,
-// lanes past head_dim idle), U of them per pass in flight from global memory.
-// A head's sums are G-lane shuffles.  Half-split pairs fetch their partner
-// elements from the lane that holds them by shuffle.
+// A warp owns a token row (WR warps share one when the rows are few).  Its
+// lanes first compute the row's angles, a few rotary pairs each, once for all q
+// and k heads: the product in fp64, reduced to [-pi, pi] by a two-part 2 pi,
+// then sin and cos of the fp32 rest, corrected to first order by what that
+// rounding dropped.  They meet in the warp's own shared memory, so nothing
+// waits for another warp.  Then G consecutive lanes own one head vector at a
+// time (16 bytes per lane; G is the next power of two, lanes past head_dim
+// idle).  A lane sees the same channels in every head: its cos and sin, with
+// gamma folded in, stay in registers for the row.  D vectors per lane are in
+// flight: as a batch of loads into registers, or, in the norm's backward pass,
+// which needs the registers for its sums and two vectors per head, through a
+// ring in shared memory that cp.async fills across the ends of heads, of q and
+// k and of rows.
+// A head's sums are G-lane shuffles, and 1/rms one factor at the end.
+// Half-split pairs fetch their partner channels as raw 32-bit words from the
+// lane that holds them.
 //
-// dgamma: each thread keeps fp32 sums of its channels over all its heads and
-// rows; the CTA joins them in a fixed order and writes one partial row.
+// dgamma: each lane keeps fp32 sums of its channels over all its heads and
+// rows (a row's in registers, added to shared memory once a row); the CTA joins
+// them in a fixed order and writes one partial row.
 //
 // Bound by HBM: forward and backward without the norm read and write every
 // head once; the backward with the norm reads dy and x and writes dx.
@@ -57,247 +65,384 @@ __device__ __forceinline__ float2 cos_sin(double pos, double freq) {
   return make_float2(fmaf(-lo, s, c), fmaf(lo, c, s));
 }
 
-// N consecutive floats of a table row (N = 2 or a multiple of 4, aligned to
-// 4 * min(N, 4) bytes).
-template <int N>
-__device__ __forceinline__ void ld_table(const float *p, float (&v)[N]) {
-  if constexpr (N == 2) {
-    const float2 t = *reinterpret_cast<const float2 *>(p);
-    v[0] = t.x;
-    v[1] = t.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 t = *reinterpret_cast<const float4 *>(p + i);
-      v[i] = t.x;
-      v[i + 1] = t.y;
-      v[i + 2] = t.z;
-      v[i + 3] = t.w;
-    }
-  }
-}
+// CTAs per SM that the registers are to leave room for: 80 registers a thread,
+// 128 in the norm's backward pass.  5 s clip, 40 + 40 heads of 128 in bf16:
+// forward with the norm 0.83 ms (64 registers: 0.87), backward 1.29 ms (80
+// registers: 2.38).
+template <int MODE>
+constexpr int kRopeMinCtas = MODE == kNormRotateBack ? 2 : 3;
+// Vectors per lane in flight.
+template <int MODE>
+constexpr int kRopeDepth = MODE == kNormRotateBack ? 6 : 4;
 
-// MODE as RopeMode.  HALF: pair i = elements (i, i + rot_dim / 2), else
-// (2i, 2i + 1).
-template <typename T, int G, bool HALF, int MODE, int U>
-__global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(
-    const __grid_constant__ RopeArgs a) {
+// MODE as RopeMode.  HALF: pair i = channels (i, i + rot_dim / 2), else
+// (2i, 2i + 1).  wr_log2: log2 of the warps that share a row.
+template <typename T, int G, bool HALF, int MODE, int D>
+__global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
+    rope_axes_kernel(const __grid_constant__ RopeArgs a, int wr_log2) {
   using IO = Io<T>;
   constexpr int E = IO::E, P = E / 2;
   constexpr bool NORM = MODE == kNormRotate || MODE == kNormRotateBack;
   constexpr bool BACK = MODE == kRotateBack || MODE == kNormRotateBack;
   constexpr bool DGAMMA = MODE == kNormRotateBack;
-  constexpr int GROUPS = kRopeThreads / G;  // head vectors per pass
+  constexpr int GW = 32 / G;                          // heads a warp holds at a time
+  constexpr int NPL = G * E / 64 > 0 ? G * E / 64 : 1;  // rotary pairs per lane, at most
+  constexpr int GROUPS = kRopeThreads / G;
   extern __shared__ __align__(16) unsigned char smem[];
 
-  const int tid = threadIdx.x;
-  const int group = tid / G, gl = tid % G;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gl = tid % G;
   const bool active = gl * E < a.head_dim;
-  const int TR = a.tile_rows;
-  // pairs of a table row: HALF one entry per rotary pair, else per element pair
-  const int npairs = HALF ? a.rot_dim / 2 : a.head_dim / 2;
-  const int pitch = (npairs + 3) & ~3;
-  float *cosb = reinterpret_cast<float *>(smem);           // [2][TR][pitch]
-  float *sinb = cosb + 2 * TR * pitch;                     // [2][TR][pitch]
-  int64_t *offs = reinterpret_cast<int64_t *>(sinb + 2 * TR * pitch);  // [2][TR][6]
+  const int half = a.rot_dim / 2;
+  // norm's backward pass: the ring (x and dy) and the lanes' dgamma sums; then
+  // each warp's cos and sin, one entry per pair (interleaved: identity pairs past
+  // rot_dim)
+  constexpr int PITCH = G * P;
+  uint4 *ring = reinterpret_cast<uint4 *>(smem) + tid;                   // [D][2][threads]
+  float2 *sums = reinterpret_cast<float2 *>(smem + (DGAMMA ? D * 2 * kRopeThreads * 16 : 0));
+  float *cosw = reinterpret_cast<float *>(sums + (DGAMMA ? 2 * P * kRopeThreads : 0)) +
+                warp * 2 * PITCH;
+  float *sinw = cosw + PITCH;
+  if constexpr (DGAMMA) {
+#pragma unroll
+    for (int m = 0; m < 2 * P; ++m) sums[m * kRopeThreads + tid] = splat2(0.f);  // [t][m][thread]
+  }
 
-  // this lane's table column, and in a half-split head its partner lane and
-  // which half it holds; lanes past rot_dim keep their elements, lanes past
-  // head_dim read column 0 and store nothing
-  int col = active ? gl * P : 0, partner = 0;
+  // this lane's first table column; half-split: the lane that holds the partner
+  // channels, and whether the lane's channels are the second of their pairs
+  int col = active ? gl * P : 0, partner = lane;
   bool second = false, turns = true;
   if constexpr (HALF) {
-    const int half = a.rot_dim / 2, e0 = gl * E;
+    const int e0 = gl * E;
     turns = e0 < a.rot_dim;
-    second = e0 >= half;
+    second = turns && e0 >= half;
     col = turns ? (second ? e0 - half : e0) : 0;
-    partner = turns ? (second ? gl - half / E : gl + half / E) : gl;
-    partner += (tid & 31) - gl;
+    if (turns) partner = second ? lane - half / E : lane + half / E;
   }
 
-  float2 gam[2][P];
-  float2 dgam[2][P];
+  // frequency and position array of the pairs this lane computes
+  double freq[NPL];
+  int64_t axis_off[NPL];
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int m = 0; m < P; ++m) {
-      gam[t][m] = splat2(1.f);
-      dgam[t][m] = splat2(0.f);
-    }
-  if constexpr (NORM) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      if (a.gamma[t] && active)
-        IO::unpack(ld_shared_vec(static_cast<const uint4 *>(a.gamma[t]) + gl), gam[t]);
+  for (int i = 0; i < NPL; ++i) {
+    const int p = lane + 32 * i;
+    freq[i] = p < half ? a.freq[p] : 0.0;
+    axis_off[i] = p < half ? a.axis[p] * a.pos_stride_axis : 0;
   }
-
-  // rotate v (elements gl*E .. of a head) by the angles of tile row `cs`;
-  // BACK turns the other way
-  auto rotate = [&](float2 (&v)[P], const float *cs, const float *sn) {
-    if constexpr (HALF) {
-      float2 w[P];
+  auto load_pos = [&](int64_t row, double (&pos)[NPL]) {
+    const unsigned b = static_cast<unsigned>(row) / static_cast<unsigned>(a.L);
+    const int64_t at =
+        b * a.pos_stride_b + (static_cast<unsigned>(row) - b * static_cast<unsigned>(a.L));
 #pragma unroll
-      for (int m = 0; m < P; ++m) {
-        w[m].x = __shfl_sync(0xffffffffu, v[m].x, partner);
-        w[m].y = __shfl_sync(0xffffffffu, v[m].y, partner);
-      }
-      // first: v cos - w sin; second: v cos + w sin
-      const float2 sg = splat2((second != BACK) ? 1.f : -1.f);
-      float c[E], s[E];
-      ld_table(cs + col, c);
-      ld_table(sn + col, s);
-      if (turns) {
-#pragma unroll
-        for (int m = 0; m < P; ++m)
-          v[m] = fma2(v[m], make_float2(c[2 * m], c[2 * m + 1]),
-                      mul2(w[m], mul2(make_float2(s[2 * m], s[2 * m + 1]), sg)));
-      }
-    } else {
-      float c[P], s[P];
-      ld_table(cs + col, c);
-      ld_table(sn + col, s);
-#pragma unroll
-      for (int m = 0; m < P; ++m) {
-        const float x = v[m].x, y = v[m].y, t = BACK ? -s[m] : s[m];
-        v[m].x = fmaf(x, c[m], -(y * t));
-        v[m].y = fmaf(x, t, y * c[m]);
-      }
+    for (int i = 0; i < NPL; ++i) {
+      if (a.pos_type == SOL_POS_I32)
+        pos[i] = static_cast<double>(__ldg(static_cast<const int *>(a.pos) + at + axis_off[i]));
+      else if (a.pos_type == SOL_POS_I64)
+        pos[i] =
+            static_cast<double>(__ldg(static_cast<const long long *>(a.pos) + at + axis_off[i]));
+      else
+        pos[i] = static_cast<double>(__ldg(static_cast<const float *>(a.pos) + at + axis_off[i]));
     }
   };
+  // identity entries past rot_dim are written once
+  if constexpr (!HALF) {
+    for (int p = half + lane; p < PITCH; p += 32) {
+      cosw[p] = 1.f;
+      sinw[p] = 0.f;
+    }
+  }
 
-  const int64_t tiles = (a.rows + TR - 1) / TR;
-  int buf = 0;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
-    const int64_t row0 = tile * TR;
-    const int nrows = a.rows - row0 < TR ? static_cast<int>(a.rows - row0) : TR;
-    float *cosr = cosb + buf * TR * pitch, *sinr = sinb + buf * TR * pitch;
-    int64_t *off = offs + buf * TR * 6;
+  const int WR = 1 << wr_log2;
+  const int rpb = (kRopeThreads / 32) >> wr_log2;            // rows of a CTA at a time
+  const int slot0 = (warp & (WR - 1)) * GW, step = WR * GW;  // heads slot0 + lane / G + i * step
+  const int slot = slot0 + lane / G;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * rpb;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * rpb + (warp >> wr_log2);
+  // passes over the heads of q and of k
+  const int passes_q = a.heads[0] > slot0 ? (a.heads[0] - slot0 + step - 1) / step : 0;
+  const int passes_k = a.heads[1] > slot0 ? (a.heads[1] - slot0 + step - 1) / step : 0;
+  if (passes_q + passes_k == 0) row = a.rows;  // more warps than heads: none for this one
 
-    for (int i = tid; i < nrows * npairs; i += kRopeThreads) {
-      const int r = i / npairs, p = i - r * npairs;
-      float2 cs = make_float2(1.f, 0.f);
-      if (2 * p < a.rot_dim) {
-        const unsigned row = static_cast<unsigned>(row0) + r, b = row / static_cast<unsigned>(a.L);
-        const int64_t at = a.axis[p] * a.pos_stride_axis + b * a.pos_stride_b +
-                           (row - b * static_cast<unsigned>(a.L));
-        double pos;
-        if (a.pos_type == SOL_POS_I32)
-          pos = static_cast<double>(__ldg(static_cast<const int *>(a.pos) + at));
-        else if (a.pos_type == SOL_POS_I64)
-          pos = static_cast<double>(__ldg(static_cast<const long long *>(a.pos) + at));
-        else
-          pos = static_cast<double>(__ldg(static_cast<const float *>(a.pos) + at));
-        cs = cos_sin(pos, a.freq[p]);
+  // The ring's producer: it walks the same rows, tensors and passes as the loop
+  // below, D - 1 vectors ahead.
+  int64_t prow = row;
+  int pt = passes_q > 0 ? 0 : 1, phead = slot, pleft = 0, pslot = 0, cons = 0;
+  const unsigned char *px = nullptr, *pg = nullptr;
+  auto seek = [&]() {
+    const unsigned b = static_cast<unsigned>(prow) / static_cast<unsigned>(a.L);
+    const unsigned r = static_cast<unsigned>(prow) - b * static_cast<unsigned>(a.L);
+    phead = slot;
+    pleft = pt == 0 ? passes_q : passes_k;
+    px = static_cast<const unsigned char *>(a.x[pt].data) +
+         (b * a.x[pt].sb + r * a.x[pt].sr + slot * a.x[pt].sh) + gl * 16;
+    pg = static_cast<const unsigned char *>(a.g[pt].data) +
+         (b * a.g[pt].sb + r * a.g[pt].sr + slot * a.g[pt].sh) + gl * 16;
+  };
+  auto produce = [&]() {
+    if (prow < a.rows) {
+      if (active && phead < a.heads[pt]) {
+        uint4 *dst = ring + pslot * (2 * kRopeThreads);
+        cp_async16(dst, px);
+        cp_async16(dst + kRopeThreads, pg);
       }
-      cosr[r * pitch + p] = cs.x;
-      sinr[r * pitch + p] = cs.y;
+      phead += step;
+      px += a.x[pt].sh * step;
+      pg += a.g[pt].sh * step;
+      if (--pleft == 0) {
+        if (pt == 0 && passes_k > 0) {
+          pt = 1;
+        } else {
+          pt = passes_q > 0 ? 0 : 1;
+          prow += stride;
+        }
+        if (prow < a.rows) seek();
+      }
     }
-    for (int i = tid; i < nrows * 6; i += kRopeThreads) {
-      const int r = i / 6, w = i - r * 6;
-      const HeadsArg &h = w < 2 ? a.x[w] : (w < 4 ? a.g[w - 2] : a.out[w - 4]);
-      const unsigned row = static_cast<unsigned>(row0) + r, b = row / static_cast<unsigned>(a.L);
-      off[r * 6 + w] = b * h.sb + (row - b * static_cast<unsigned>(a.L)) * h.sr;
-    }
-    __syncthreads();
+    cp_async_commit();
+    pslot = pslot + 1 == D ? 0 : pslot + 1;
+  };
+  if constexpr (DGAMMA) {
+    if (prow < a.rows) seek();
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) produce();
+  }
 
+  double pos[NPL];
+  if (row < a.rows) load_pos(row, pos);
+  for (; row < a.rows; row += stride) {
+    const unsigned b = static_cast<unsigned>(row) / static_cast<unsigned>(a.L);
+    const unsigned r = static_cast<unsigned>(row) - b * static_cast<unsigned>(a.L);
+    __syncwarp();  // every lane has read the previous row's table
 #pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const int p = lane + 32 * i;
+      if (p < half) {
+        const float2 cs = cos_sin(pos[i], freq[i]);
+        cosw[p] = cs.x;
+        sinw[p] = cs.y;
+      }
+    }
+    __syncwarp();
+    if (row + stride < a.rows) load_pos(row + stride, pos);
+
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
-      const int heads = a.heads[t];
-      const int items = nrows * heads;
-      const unsigned char *xin = static_cast<const unsigned char *>(a.x[t].data) + gl * 16;
-      const unsigned char *gin = static_cast<const unsigned char *>(a.g[t].data) + gl * 16;
-      unsigned char *out = static_cast<unsigned char *>(a.out[t].data) + gl * 16;
-      for (int base = group; base - group < items; base += GROUPS * U) {
-        uint4 vx[U], vg[U];
-        int row[U], head[U];
+      const int passes = t == 0 ? passes_q : passes_k;
+      if (passes == 0) continue;
+      float2 dg[P];  // this row's part of dgam[t]
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = base + u * GROUPS;
-          row[u] = heads == 1 ? i
-                              : static_cast<int>(__umulhi(static_cast<unsigned>(i), a.magic[t]));
-          head[u] = i - row[u] * heads;
-          vx[u] = make_uint4(0, 0, 0, 0);
-          vg[u] = make_uint4(0, 0, 0, 0);
-          if (i < items && active) {
-            if constexpr (MODE != kRotateBack)
-              vx[u] = ld_head16(xin + off[row[u] * 6 + t] + head[u] * a.x[t].sh);
-            if constexpr (BACK)
-              vg[u] = ld_head16(gin + off[row[u] * 6 + 2 + t] + head[u] * a.g[t].sh);
+      for (int m = 0; m < P; ++m) dg[m] = splat2(0.f);
+      // cos, sin and gamma of the lane's channels (gp: its partner channels)
+      float2 c[P], s[P], gam[P], gp[P];
+#pragma unroll
+      for (int m = 0; m < P; ++m) gam[m] = gp[m] = splat2(1.f);
+      if constexpr (NORM) {
+        if (a.gamma[t]) {
+          uint4 raw = make_uint4(0, 0, 0, 0);
+          if (active) raw = ld_shared_vec(static_cast<const uint4 *>(a.gamma[t]) + gl);
+          uint4 rp = raw;
+          if constexpr (HALF && !BACK) {
+            rp.x = __shfl_sync(0xffffffffu, raw.x, partner);
+            rp.y = __shfl_sync(0xffffffffu, raw.y, partner);
+            rp.z = __shfl_sync(0xffffffffu, raw.z, partner);
+            rp.w = __shfl_sync(0xffffffffu, raw.w, partner);
+          }
+          IO::unpack(raw, gam);
+          IO::unpack(rp, gp);
+        }
+      }
+      // the turn of one component pair (u, v) held as A, B:
+      //   interleaved forward   even = e A - o B,  odd = e C + o D
+      //   interleaved backward  even = e c + o s,  odd = o c - e s
+      //   half-split            out = own A + partner B
+      float2 A[P], B[P];
+      if constexpr (HALF) {
+#pragma unroll
+        for (int m = 0; m < P; ++m) {
+          c[m] = turns ? *reinterpret_cast<const float2 *>(cosw + col + 2 * m) : splat2(1.f);
+          s[m] = turns ? *reinterpret_cast<const float2 *>(sinw + col + 2 * m) : splat2(0.f);
+          const float sg = (second != BACK) ? 1.f : -1.f;
+          A[m] = BACK ? c[m] : mul2(c[m], gam[m]);
+          B[m] = mul2(s[m], splat2(sg));
+          if constexpr (!BACK) B[m] = mul2(B[m], gp[m]);
+        }
+      } else {
+        // entry m: pairs 2m and 2m + 1 of the lane; first P/2 entries of A, B for
+        // the even outputs, the others for the odd ones
+#pragma unroll
+        for (int m = 0; m < P / 2; ++m) {
+          c[m] = *reinterpret_cast<const float2 *>(cosw + col + 2 * m);
+          s[m] = *reinterpret_cast<const float2 *>(sinw + col + 2 * m);
+          const float2 ge = make_float2(gam[2 * m].x, gam[2 * m + 1].x);
+          const float2 go = make_float2(gam[2 * m].y, gam[2 * m + 1].y);
+          if constexpr (BACK) {
+            A[m] = c[m];
+            B[m] = s[m];
+          } else {
+            A[m] = mul2(c[m], ge);                              // even from even
+            B[m] = mul2(mul2(s[m], go), splat2(-1.f));          // even from odd
+            A[m + P / 2] = mul2(c[m], go);                      // odd from odd
+            B[m + P / 2] = mul2(s[m], ge);                      // odd from even
+          }
+          gam[2 * m] = ge;  // kept in the same split as the channels
+          gam[2 * m + 1] = go;
+        }
+      }
+
+      // one head vector (dy with it in the norm's backward pass) to dst
+      auto turn = [&](uint4 vx, uint4 vg, bool live, unsigned char *dst) {
+        // v: the vector that is turned; o: the turned one
+        const uint4 v = BACK ? vg : vx;
+        float2 o[P];
+        if constexpr (HALF) {
+          uint4 vp;
+          vp.x = __shfl_sync(0xffffffffu, v.x, partner);
+          vp.y = __shfl_sync(0xffffffffu, v.y, partner);
+          vp.z = __shfl_sync(0xffffffffu, v.z, partner);
+          vp.w = __shfl_sync(0xffffffffu, v.w, partner);
+          float2 own[P], oth[P];
+          IO::unpack(v, own);
+          IO::unpack(vp, oth);
+#pragma unroll
+          for (int m = 0; m < P; ++m) o[m] = fma2(own[m], A[m], mul2(oth[m], B[m]));
+        } else {
+          float2 ev[P / 2], od[P / 2];
+          IO::unpack_eo(v, ev, od);
+#pragma unroll
+          for (int m = 0; m < P / 2; ++m) {
+            if constexpr (BACK) {
+              const float2 neg = mul2(B[m], splat2(-1.f));
+              o[2 * m] = fma2(ev[m], A[m], mul2(od[m], B[m]));
+              o[2 * m + 1] = fma2(od[m], A[m], mul2(ev[m], neg));
+            } else {
+              o[2 * m] = fma2(ev[m], A[m], mul2(od[m], B[m]));
+              o[2 * m + 1] = fma2(od[m], A[m + P / 2], mul2(ev[m], B[m + P / 2]));
+            }
           }
         }
+        if constexpr (NORM) {
+          float2 x[P];
+          if constexpr (HALF) {
+            IO::unpack(vx, x);
+          } else {
+            float2 ev[P / 2], od[P / 2];
+            IO::unpack_eo(vx, ev, od);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = base + u * GROUPS;
-          const bool live = i < items;
-          const int r = live ? row[u] : 0;
-          const float *cs = cosr + r * pitch, *sn = sinr + r * pitch;
-          float2 x[P], g[P];
-          if constexpr (MODE != kRotateBack) IO::unpack(vx[u], x);
-          if constexpr (BACK) {
-            IO::unpack(vg[u], g);
-            rotate(g, cs, sn);
+            for (int m = 0; m < P / 2; ++m) {
+              x[2 * m] = ev[m];
+              x[2 * m + 1] = od[m];
+            }
           }
-          if constexpr (NORM) {
-            float2 sq = splat2(0.f), dot = splat2(0.f);
+          float2 sq = splat2(0.f), dot = splat2(0.f), h[P];
+#pragma unroll
+          for (int m = 0; m < P; ++m) {
+            sq = fma2(x[m], x[m], sq);
+            if constexpr (BACK) {
+              h[m] = mul2(o[m], gam[m]);
+              dot = fma2(h[m], x[m], dot);
+            }
+          }
+          float ss = sq.x + sq.y, d = dot.x + dot.y;
+#pragma unroll
+          for (int w = G / 2; w > 0; w >>= 1) {
+            ss += __shfl_xor_sync(0xffffffffu, ss, w);
+            if constexpr (BACK) d += __shfl_xor_sync(0xffffffffu, d, w);
+          }
+          const float rstd = rsqrtf(fmaf(ss, a.inv_hd, a.eps));
+          const float2 r2 = splat2(rstd);
+          if constexpr (BACK) {
+            // x^ = x rstd;  dx = rstd (h - x^ mean(x^ h))
+            const float2 k2 = splat2(-rstd * rstd * d * a.inv_hd);
 #pragma unroll
             for (int m = 0; m < P; ++m) {
-              sq = fma2(x[m], x[m], sq);
-              if constexpr (BACK) dot = fma2(mul2(x[m], gam[t][m]), g[m], dot);
+              x[m] = mul2(x[m], r2);
+              if (live) dg[m] = fma2(o[m], x[m], dg[m]);
+              o[m] = fma2(x[m], k2, mul2(h[m], r2));
             }
-            float s = sq.x + sq.y, d = dot.x + dot.y;
+          } else {
 #pragma unroll
-            for (int o = G / 2; o > 0; o >>= 1) {
-              s += __shfl_xor_sync(0xffffffffu, s, o);
-              if constexpr (BACK) d += __shfl_xor_sync(0xffffffffu, d, o);
-            }
-            const float rstd = rsqrtf(fmaf(s, a.inv_hd, a.eps));
-            const float2 r2 = splat2(rstd);
-            if constexpr (BACK) {
-              // dx = rstd * (gamma g) - x * rstd^3 * mean(x gamma g)
-              const float2 k2 = splat2(-rstd * rstd * rstd * d * a.inv_hd);
-#pragma unroll
-              for (int m = 0; m < P; ++m) {
-                if (live) dgam[t][m] = fma2(g[m], mul2(x[m], r2), dgam[t][m]);
-                g[m] = fma2(x[m], k2, mul2(mul2(gam[t][m], g[m]), r2));
-              }
-            } else {
-#pragma unroll
-              for (int m = 0; m < P; ++m) x[m] = mul2(mul2(x[m], r2), gam[t][m]);
-            }
+            for (int m = 0; m < P; ++m) o[m] = mul2(o[m], r2);
           }
-          if constexpr (!BACK) rotate(x, cs, sn);
-          if (live && active) {
-            unsigned char *dst = out + off[r * 6 + 4 + t] + head[u] * a.out[t].sh;
-            if constexpr (BACK)
-              st_stream16(dst, IO::pack(g));
-            else
-              st_stream16(dst, IO::pack(x));
+        }
+        if (live) {
+          uint4 res;
+          if constexpr (HALF) {
+            res = IO::pack(o);
+          } else {
+            float2 ev[P / 2], od[P / 2];
+#pragma unroll
+            for (int m = 0; m < P / 2; ++m) {
+              ev[m] = o[2 * m];
+              od[m] = o[2 * m + 1];
+            }
+            res = IO::pack_eo(ev, od);
           }
+          st_stream16(dst, res);
+        }
+      };
+      unsigned char *out = static_cast<unsigned char *>(a.out[t].data) +
+                           (b * a.out[t].sb + r * a.out[t].sr + slot * a.out[t].sh) + gl * 16;
+      const int64_t ostep = a.out[t].sh * step;
+      int head = slot;
+      if constexpr (DGAMMA) {
+#pragma unroll 1
+        for (int i = 0; i < passes; ++i, head += step, out += ostep) {
+          produce();
+          cp_async_wait<D - 1>();
+          const uint4 *entry = ring + cons * (2 * kRopeThreads);
+          cons = cons + 1 == D ? 0 : cons + 1;
+          const bool live = active && head < a.heads[t];
+          uint4 vx = make_uint4(0, 0, 0, 0), vg = make_uint4(0, 0, 0, 0);
+          if (live) {
+            vx = entry[0];
+            vg = entry[kRopeThreads];
+          }
+          turn(vx, vg, live, out);
+        }
+      } else {
+        const HeadsArg &in = BACK ? a.g[t] : a.x[t];
+        const unsigned char *src = static_cast<const unsigned char *>(in.data) +
+                                   (b * in.sb + r * in.sr + slot * in.sh) + gl * 16;
+        const int64_t istep = in.sh * step;
+        for (int i = 0; i < passes; i += D, head += D * step) {
+          uint4 v[D];
+#pragma unroll
+          for (int u = 0; u < D; ++u) {
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (active && head + u * step < a.heads[t]) v[u] = ld_head16(src + u * istep);
+          }
+          src += D * istep;
+#pragma unroll
+          for (int u = 0; u < D; ++u)
+            if (i + u < passes)  // the same for the whole warp
+              turn(v[u], v[u], active && head + u * step < a.heads[t], out + u * ostep);
+          out += D * ostep;
+        }
+      }
+      if constexpr (DGAMMA) {
+#pragma unroll
+        for (int m = 0; m < P; ++m) {
+          float2 *sum = sums + (t * P + m) * kRopeThreads + tid;
+          *sum = add2(*sum, dg[m]);
         }
       }
     }
   }
-
   if constexpr (DGAMMA) {
+    cp_async_wait<0>();
     if (a.partial) {
-      // [group][channel]: the groups' sums, added in order by one thread per
-      // channel of q and k
+      // channel c of q and k: the groups' sums, added in order by one thread
       __syncthreads();
-      float *park = reinterpret_cast<float *>(smem);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (active) {
-#pragma unroll
-          for (int m = 0; m < P; ++m)
-            reinterpret_cast<float2 *>(park + group * a.head_dim + gl * E)[m] = dgam[t][m];
-        }
-        __syncthreads();
-        for (int c = tid; c < a.head_dim; c += kRopeThreads) {
-          float s = 0.f;
-          for (int y = 0; y < GROUPS; ++y) s += park[y * a.head_dim + c];
-          a.partial[(static_cast<int64_t>(blockIdx.x) * 2 + t) * a.head_dim + c] = s;
-        }
-        __syncthreads();
+      for (int i = tid; i < 2 * a.head_dim; i += kRopeThreads) {
+        const int t = i >= a.head_dim ? 1 : 0, c = i - t * a.head_dim;
+        // where the lane of channel c keeps it: float2 entry and component
+        const int e = c % E;
+        const int m = HALF ? e / 2 : 2 * (e / 4) + (e & 1);
+        const int comp = HALF ? e & 1 : (e / 2) & 1;
+        const float2 *p = sums + (t * P + m) * kRopeThreads + c / E;
+        float s = 0.f;
+        for (int y = 0; y < GROUPS; ++y) s += comp ? p[y * G].y : p[y * G].x;
+        a.partial[(static_cast<int64_t>(blockIdx.x) * 2 + t) * a.head_dim + c] = s;
       }
     }
   }
@@ -305,33 +450,28 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(
 
 template <typename T, int G, bool HALF, int MODE>
 cudaError_t launch_t(RopeArgs &a, cudaStream_t stream, int *ctas) {
-  constexpr int U = 4;
-  constexpr int GROUPS = kRopeThreads / G;
-  auto *kern = &rope_axes_kernel<T, G, HALF, MODE, U>;
-  const int npairs = HALF ? a.rot_dim / 2 : a.head_dim / 2;
-  const int pitch = (npairs + 3) & ~3;
-  const int heads = a.heads[0] + a.heads[1];
+  constexpr bool DGAMMA = MODE == kNormRotateBack;
+  constexpr int D = kRopeDepth<MODE>;
+  constexpr int GW = 32 / G, WARPS = kRopeThreads / 32;
+  auto *kern = &rope_axes_kernel<T, G, HALF, MODE, D>;
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidConfiguration;
-  // Rows per tile: one angle per thread at least, and enough heads for a full
-  // pass of U vectors per thread; fewer while the rows would leave SMs idle.
-  int tr = kRopeThreads / npairs;
-  if (tr < 1) tr = 1;
-  while (tr < 32 && tr * heads < GROUPS * U) tr *= 2;
-  if (tr > 32) tr = 32;
-  while (tr > 1 && (a.rows + tr - 1) / tr < 2 * sms) tr /= 2;
-  a.tile_rows = tr;
-  size_t smem = static_cast<size_t>(tr) * (4 * pitch * 4 + 2 * 6 * 8);
-  const size_t park = static_cast<size_t>(GROUPS) * a.head_dim * 4;
-  if (MODE == kNormRotateBack && a.partial && smem < park) smem = park;
+  // Warps per row: one while that fills the SMs, more while rows are few and
+  // heads are left to share.
+  const int heads = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
+  int wr = 0;
+  while ((1 << wr) < WARPS && (GW << wr) < heads && (a.rows << wr) < 16LL * sms) ++wr;
+  constexpr int PITCH = G * Io<T>::E / 2;
+  const size_t smem = (DGAMMA ? static_cast<size_t>(kRopeThreads) * (D * 32 + Io<T>::E * 8) : 0) +
+                      static_cast<size_t>(WARPS) * 2 * PITCH * 4;
   const int per_sm = resident_blocks(reinterpret_cast<const void *>(kern), kRopeThreads, smem);
   if (per_sm <= 0) return cudaErrorInvalidConfiguration;
   int64_t grid = static_cast<int64_t>(per_sm) * sms;
-  const int64_t tiles = (a.rows + tr - 1) / tr;
-  if (grid > tiles) grid = tiles;
+  const int64_t most = ((a.rows << wr) + WARPS - 1) / WARPS;
+  if (grid > most) grid = most;
   if (grid > kMaxRopeCtas) grid = kMaxRopeCtas;
   *ctas = static_cast<int>(grid);
-  kern<<<static_cast<unsigned>(grid), kRopeThreads, smem, stream>>>(a);
+  kern<<<static_cast<unsigned>(grid), kRopeThreads, smem, stream>>>(a, wr);
   return cudaGetLastError();
 }
 

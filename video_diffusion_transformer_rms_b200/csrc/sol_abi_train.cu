@@ -95,12 +95,6 @@ sol_status check_workspace(const char *fn, const void *ws, size_t bytes, size_t 
   return check_aligned(fn, {ws});
 }
 
-// Slots of the row sums: shares + keys.
-size_t sum_slots(int64_t B, int64_t L) {
-  const int64_t rows = B * L;
-  return static_cast<size_t>((rows < kMaxSumCtas ? rows : kMaxSumCtas) + 2 * B);
-}
-
 bool sizes_ok(int64_t B, int64_t L, int64_t D) {
   return B >= 0 && L >= 0 && D > 0 && B <= kMaxRows && L <= kMaxRows && B * L <= kMaxRows &&
          D <= kMaxRowBytesRms / 2;
@@ -326,9 +320,6 @@ sol_status rope_args(const char *fn, const sol_rope_plan *plan, const sol_positi
       return fail(SOL_ERR_UNSUPPORTED, "%s: 1 to %lld heads (got %lld)", fn,
                   (long long)kMaxRopeHeads, (long long)out[t]->n_heads);
     a.heads[t] = static_cast<int>(out[t]->n_heads);
-    a.magic[t] = a.heads[t] > 1
-                     ? static_cast<uint32_t>(((1ull << 32) + a.heads[t] - 1) / a.heads[t])
-                     : 0;
   }
   if (!out[1] && gamma_k)
     return fail(SOL_ERR_INVALID_ARG, "%s: gamma_k without k", fn);
@@ -482,12 +473,12 @@ sol_status sol_layer_norm(const void *x, void *y, float *mean, float *rstd, cons
 
 size_t sol_norm_backward_workspace_bytes(int64_t B, int64_t L, int64_t D) {
   if (!sizes_ok(B, L, D)) return 0;
-  return sum_slots(B, L) * 2 * static_cast<size_t>(D) * 4;
+  return static_cast<size_t>(sum_slots(B * L, 2 * B)) * 2 * static_cast<size_t>(D) * 4;
 }
 
 size_t sol_dropout_backward_workspace_bytes(int64_t B, int64_t L, int64_t D) {
   if (!sizes_ok(B, L, D)) return 0;
-  return sum_slots(B, L) * static_cast<size_t>(D) * 4;
+  return static_cast<size_t>(sum_slots(B * L, 2 * B)) * static_cast<size_t>(D) * 4;
 }
 
 sol_status sol_layer_norm_backward(const void *dy, const void *x, const float *mean,

@@ -47,6 +47,10 @@ struct Segments {
 };
 // Bound on `ctas`: four CTAs on each of 148 SMs.
 constexpr int kMaxSumCtas = 592;
+// Slots of the workspace: shares and keys.
+inline int64_t sum_slots(int64_t rows, int64_t keys) {
+  return (rows < kMaxSumCtas ? rows : kMaxSumCtas) + keys;
+}
 
 struct SumArgs {
   Segments seg;
@@ -118,14 +122,12 @@ struct RopeArgs {
   HeadsArg g[2];       // backward: gradients of the outputs
   HeadsArg out[2];     // forward: outputs; backward: gradients of the inputs
   int heads[2];
-  uint32_t magic[2];   // heads > 1: ceil(2^32 / heads), i / heads = (i * magic) >> 32
   const void *gamma[2];
   const void *pos;
   int64_t pos_stride_axis, pos_stride_b;  // elements
   int pos_type;        // sol_pos_type
   int L;
   int64_t rows;
-  int tile_rows;       // set by the launcher
   int head_dim, rot_dim;
   float eps;
   float inv_hd;

@@ -507,7 +507,7 @@ sol_status sol_layer_norm(const void *x, void *y, float *mean, float *rstd,
  *                 scale.
  *   workspace     sol_norm_backward_workspace_bytes; may be NULL when no
  *                 gradient of a vector is wanted.
- *   With scale, B <= 32767.  n_video, D as for sol_rms_adaln.
+ *   n_video, D    as for sol_rms_adaln.
  */
 sol_status sol_layer_norm_backward(
     const void *dy, const void *x, const float *mean, const float *rstd,
@@ -588,7 +588,7 @@ sol_status sol_dropout_residual(const void *h, const void *branch,
  *   rng, site, p  those of the forward call.
  *   workspace     sol_dropout_backward_workspace_bytes; may be NULL if dgate
  *                 is.
- *   With dgate, B <= 32767.  p = 0 gives the gradient of sol_gate_residual.
+ *   p = 0 gives the gradient of sol_gate_residual.
  */
 sol_status sol_dropout_residual_backward(
     const void *dout, const void *branch, const void *gate, void *dbranch,

@@ -322,25 +322,61 @@ def gemm_gelu(A: torch.Tensor, B: torch.Tensor, bias: Optional[torch.Tensor] = N
 _NO_CONTEXT = contextlib.nullcontext()
 
 
+# These wrappers are the whole cost of a small call, so an operand is checked
+# and turned into its address in one step.
+
+def _arg(t: Optional[torch.Tensor], shape, name: str, like: torch.Tensor, dtype=None):
+    """Address of a contiguous operand of this shape, on the device of `like`
+    and of its dtype (or of the one given); None for None."""
+    if t is None:
+        return None
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got "
+                         f"{tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name} is on {t.device}, the inputs on {like.device}")
+    if dtype is None:
+        if t.dtype is not like.dtype:
+            raise TypeError(f"all tensors must share one dtype, got {t.dtype} for {name} and "
+                            f"{like.dtype}")
+    elif t.dtype is not dtype:
+        raise TypeError(f"{name} must be {str(dtype).split('.')[1]}, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _io_dtype(t: torch.Tensor) -> int:
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"dtype {t.dtype} is not supported (float32 or bfloat16)")
+    return dt
+
+
 def _on(t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
     """The context a call on `t` runs in: t's device is current, and `stream`,
     where one is given, is the current stream, so that outputs and workspaces
     allocated inside belong to the stream that uses them."""
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("libsol takes CUDA tensors")
     if stream is not None:
         if stream.device != t.device:
             raise ValueError(f"the stream is on {stream.device}, the inputs on {t.device}")
         return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
+    if dev != torch._C._cuda_getDevice():
+        return torch.cuda.device(dev)
     return _NO_CONTEXT
+
+
+def _current(t: torch.Tensor) -> int:
+    """Handle of the current stream of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _workspace(given: Optional[torch.Tensor], need: int, like: torch.Tensor) -> torch.Tensor:
     if given is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
-    _expect(given, given.shape, "workspace", like)
+        return torch.empty_strided((need if need > 16 else 16,), (1,), dtype=torch.uint8,
+                                   device=like.device)
+    _arg(given, given.shape, "workspace", like, given.dtype)
     return given
 
 
@@ -351,8 +387,17 @@ def _rows3(x: torch.Tensor, n_video: Optional[int], name: str):
     return B, L, D, L if n_video is None else n_video
 
 
-def _fp32(shape, like: torch.Tensor) -> torch.Tensor:
-    return torch.empty(shape, dtype=torch.float32, device=like.device)
+def _fp32(shape, stride, like: torch.Tensor) -> torch.Tensor:
+    # (the cheapest of PyTorch's allocation calls by about 1 us)
+    return torch.empty_strided(shape, stride, dtype=torch.float32, device=like.device)
+
+
+def _packed(t: torch.Tensor) -> torch.Tensor:
+    """An uninitialised contiguous [B, L, H, hd] tensor like t, whose strides may
+    be any."""
+    B, L, H, hd = t.shape
+    return torch.empty_strided((B, L, H, hd), (L * H * hd, H * hd, hd, 1), dtype=t.dtype,
+                               device=t.device)
 
 
 def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
@@ -366,18 +411,22 @@ def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
     None.  Returns (y, mean, rstd); the statistics, fp32 [B, L], are what
     layer_norm_backward takes, and None with stats=False."""
     B, L, D, nv = _rows3(x, n_video, "x")
-    for t, shape, name in ((gamma, (D,), "gamma"), (beta, (D,), "beta"),
-                           (scale, (B, 2, D), "scale"), (shift, (B, 2, D), "shift"),
-                           (out, (B, L, D), "out")):
-        _expect(t, shape, name, x)
-    dt = _dtype(x, gamma, beta, scale, shift, out)
+    vec, mod = (D,), (B, 2, D)
+    args = (_arg(gamma, vec, "gamma", x), _arg(beta, vec, "beta", x),
+            _arg(scale, mod, "scale", x), _arg(shift, mod, "shift", x))
+    py = _arg(out, x.shape, "out", x)
+    dt = _io_dtype(x)
     with _on(x, stream):
-        y = torch.empty_like(x) if out is None else out
-        mean = _fp32((B, L), x) if stats else None
-        rstd = _fp32((B, L), x) if stats else None
-        _abi.check(_abi.sol_layer_norm(_ptr(x), _ptr(y), _ptr(mean), _ptr(rstd), _ptr(gamma),
-                                       _ptr(beta), _ptr(scale), _ptr(shift), B, L, nv, D, eps,
-                                       dt, _stream(None)))
+        y = out
+        if y is None:
+            y = torch.empty_like(x)
+            py = y.data_ptr()
+        mean = rstd = pm = pr = None
+        if stats:
+            mean, rstd = _fp32((B, L), (L, 1), x), _fp32((B, L), (L, 1), x)
+            pm, pr = mean.data_ptr(), rstd.data_ptr()
+        _abi.check(_abi.sol_layer_norm(x.data_ptr(), py, pm, pr, *args, B, L, nv, D, eps, dt,
+                                       _current(x)))
     return y, mean, rstd
 
 
@@ -403,26 +452,31 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     added to dx.  dx may be dy, x or dres (in place).  The workspace
     (sol_norm_backward_workspace_bytes) is allocated by PyTorch unless given."""
     B, L, D, nv = _rows3(x, n_video, "x")
-    for t, shape, name in ((dy, (B, L, D), "dy"), (mean, (B, L), "mean"), (rstd, (B, L), "rstd"),
-                           (gamma, (D,), "gamma"), (beta, (D,), "beta"),
-                           (scale, (B, 2, D), "scale"), (dres, (B, L, D), "dres"),
-                           (dx, (B, L, D), "dx")):
-        _expect(t, shape, name, x)
-    if mean.dtype != torch.float32 or rstd.dtype != torch.float32:
-        raise TypeError("mean and rstd must be float32")
-    dt = _dtype(x, dy, gamma, beta, scale, dres, dx)
+    shape, rows, vec, mod = x.shape, (B, L), (D,), (B, 2, D)
+    args = (_arg(dy, shape, "dy", x), x.data_ptr(), _arg(mean, rows, "mean", x, torch.float32),
+            _arg(rstd, rows, "rstd", x, torch.float32), _arg(gamma, vec, "gamma", x),
+            _arg(beta, vec, "beta", x), _arg(scale, mod, "scale", x),
+            _arg(dres, shape, "dres", x))
+    pd = _arg(dx, shape, "dx", x)
+    dt = _io_dtype(x)
     with _on(x, stream):
-        d = torch.empty_like(x) if dx is None else dx
-        dgamma = None if gamma is None else _fp32((D,), x)
-        dbeta = None if beta is None else _fp32((D,), x)
-        dscale = None if scale is None else _fp32((B, 2, D), x)
-        dshift = None if scale is None else _fp32((B, 2, D), x)
+        if dx is None:
+            dx = torch.empty_like(x)
+            pd = dx.data_ptr()
+        dgamma = dbeta = dscale = dshift = pg = pb = ps = ph = None
+        if gamma is not None:
+            dgamma = _fp32(vec, (1,), x)
+            pg = dgamma.data_ptr()
+        if beta is not None:
+            dbeta = _fp32(vec, (1,), x)
+            pb = dbeta.data_ptr()
+        if scale is not None:
+            dscale, dshift = _fp32(mod, (2 * D, D, 1), x), _fp32(mod, (2 * D, D, 1), x)
+            ps, ph = dscale.data_ptr(), dshift.data_ptr()
         ws = _workspace(workspace, _abi.sol_norm_backward_workspace_bytes(B, L, D), x)
         _abi.check(_abi.sol_layer_norm_backward(
-            _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(beta), _ptr(scale),
-            _ptr(dres), _ptr(d), _ptr(dgamma), _ptr(dbeta), _ptr(dscale), _ptr(dshift), B, L, nv,
-            D, _ptr(ws), ws.numel() * ws.element_size(), dt, _stream(None)))
-    return NormGrads(d, dgamma, dbeta, dscale, dshift)
+            *args, pd, pg, pb, ps, ph, B, L, nv, D, ws.data_ptr(), ws.nbytes, dt, _current(x)))
+    return NormGrads(dx, dgamma, dbeta, dscale, dshift)
 
 
 def rms_adaln_backward(dy: torch.Tensor, x: torch.Tensor, scale: torch.Tensor, n_video: int,
@@ -436,31 +490,34 @@ def rms_adaln_backward(dy: torch.Tensor, x: torch.Tensor, scale: torch.Tensor, n
     n_video, gamma, eps) for dy; those of vectors fp32, dgamma None without
     gamma.  dres, dx and workspace as for layer_norm_backward."""
     B, L, D, nv = _rows3(x, n_video, "x")
-    for t, shape, name in ((dy, (B, L, D), "dy"), (scale, (B, 2, D), "scale"),
-                           (gamma, (D,), "gamma"), (dres, (B, L, D), "dres"),
-                           (dx, (B, L, D), "dx")):
-        _expect(t, shape, name, x)
-    dt = _dtype(x, dy, scale, gamma, dres, dx)
+    shape = x.shape
+    args = (_arg(dy, shape, "dy", x), x.data_ptr(), _arg(scale, (B, 2, D), "scale", x),
+            _arg(gamma, (D,), "gamma", x), _arg(dres, shape, "dres", x))
+    pd = _arg(dx, shape, "dx", x)
+    dt = _io_dtype(x)
     with _on(x, stream):
-        d = torch.empty_like(x) if dx is None else dx
-        dscale, dshift = _fp32((B, 2, D), x), _fp32((B, 2, D), x)
-        dgamma = None if gamma is None else _fp32((D,), x)
+        if dx is None:
+            dx = torch.empty_like(x)
+            pd = dx.data_ptr()
+        mod, stride = (B, 2, D), (2 * D, D, 1)
+        dscale, dshift = _fp32(mod, stride, x), _fp32(mod, stride, x)
+        dgamma = None if gamma is None else _fp32((D,), (1,), x)
         ws = _workspace(workspace, _abi.sol_norm_backward_workspace_bytes(B, L, D), x)
         _abi.check(_abi.sol_rms_adaln_backward(
-            _ptr(dy), _ptr(x), _ptr(scale), _ptr(gamma), _ptr(dres), _ptr(d), _ptr(dscale),
-            _ptr(dshift), _ptr(dgamma), B, L, nv, D, eps, _ptr(ws),
-            ws.numel() * ws.element_size(), dt, _stream(None)))
-    return d, dscale, dshift, dgamma
+            *args, pd, dscale.data_ptr(), dshift.data_ptr(),
+            None if gamma is None else dgamma.data_ptr(), B, L, nv, D, eps, ws.data_ptr(),
+            ws.nbytes, dt, _current(x)))
+    return dx, dscale, dshift, dgamma
 
 
-def _check_rng(rng: Optional[torch.Tensor], p: float, like: torch.Tensor):
+def _rng_arg(rng: Optional[torch.Tensor], p: float, like: torch.Tensor):
     if rng is None:
         if p != 0:
             raise ValueError("rng is needed with p > 0")
-        return
-    _expect(rng, (2,), "rng", like)
-    if rng.dtype not in (torch.int64, torch.uint64):
+        return None
+    if rng.dtype is not torch.int64 and rng.dtype is not torch.uint64:
         raise TypeError("rng must be int64 or uint64: (seed, offset)")
+    return _arg(rng, (2,), "rng", like, rng.dtype)
 
 
 def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], site: int = 0,
@@ -472,18 +529,20 @@ def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], site: int = 
     gradient is dropout(dout, p, rng, site)."""
     if x.dim() < 1 or not x.is_contiguous():
         raise ValueError("x must be a contiguous tensor")
-    _expect(out, x.shape, "out", x)
-    _check_rng(rng, p, x)
+    po = _arg(out, x.shape, "out", x)
+    prng = _rng_arg(rng, p, x)
     D = x.shape[-1]
     rows = x.numel() // D if D else 0
-    dt = _dtype(x, out)
+    dt = _io_dtype(x)
     with _on(x, stream):
-        o = torch.empty_like(x) if out is None else out
-        if x.numel():
-            _abi.check(_abi.sol_dropout_residual(None, _ptr(x), None, _ptr(o), _ptr(rng),
+        if out is None:
+            out = torch.empty_like(x)
+            po = out.data_ptr()
+        if rows:
+            _abi.check(_abi.sol_dropout_residual(None, x.data_ptr(), None, po, prng,
                                                  site % 2**64, p, 1, rows, rows, D, dt,
-                                                 _stream(None)))
-    return o
+                                                 _current(x)))
+    return out
 
 
 def dropout_residual(h: Optional[torch.Tensor], branch: torch.Tensor,
@@ -495,17 +554,18 @@ def dropout_residual(h: Optional[torch.Tensor], branch: torch.Tensor,
     [B, 2, D] (None for 1; h None for 0).  rng and site as for dropout; no mask
     is stored.  out may be h or branch (in place)."""
     B, L, D, nv = _rows3(branch, n_video, "branch")
-    for t, shape, name in ((h, (B, L, D), "h"), (gate, (B, 2, D), "gate"),
-                           (out, (B, L, D), "out")):
-        _expect(t, shape, name, branch)
-    _check_rng(rng, p, branch)
-    dt = _dtype(branch, h, gate, out)
+    ph = _arg(h, branch.shape, "h", branch)
+    pg = _arg(gate, (B, 2, D), "gate", branch)
+    po = _arg(out, branch.shape, "out", branch)
+    prng = _rng_arg(rng, p, branch)
+    dt = _io_dtype(branch)
     with _on(branch, stream):
-        o = torch.empty_like(branch) if out is None else out
-        _abi.check(_abi.sol_dropout_residual(_ptr(h), _ptr(branch), _ptr(gate), _ptr(o),
-                                             _ptr(rng), site % 2**64, p, B, L, nv, D, dt,
-                                             _stream(None)))
-    return o
+        if out is None:
+            out = torch.empty_like(branch)
+            po = out.data_ptr()
+        _abi.check(_abi.sol_dropout_residual(ph, branch.data_ptr(), pg, po, prng, site % 2**64,
+                                             p, B, L, nv, D, dt, _current(branch)))
+    return out
 
 
 def dropout_residual_backward(dout: torch.Tensor, branch: Optional[torch.Tensor],
@@ -522,22 +582,25 @@ def dropout_residual_backward(dout: torch.Tensor, branch: Optional[torch.Tensor]
     B, L, D, nv = _rows3(dout, n_video, "dout")
     if gate is not None and branch is None:
         raise ValueError("branch is needed for the gradient of gate")
-    for t, shape, name in ((branch, (B, L, D), "branch"), (gate, (B, 2, D), "gate"),
-                           (dbranch, (B, L, D), "dbranch")):
-        _expect(t, shape, name, dout)
-    _check_rng(rng, p, dout)
-    dt = _dtype(dout, branch, gate, dbranch)
+    pb = _arg(branch, dout.shape, "branch", dout)
+    pg = _arg(gate, (B, 2, D), "gate", dout)
+    pd = _arg(dbranch, dout.shape, "dbranch", dout)
+    prng = _rng_arg(rng, p, dout)
+    dt = _io_dtype(dout)
     with _on(dout, stream):
-        d = torch.empty_like(dout) if dbranch is None else dbranch
-        dgate = ws = None
+        if dbranch is None:
+            dbranch = torch.empty_like(dout)
+            pd = dbranch.data_ptr()
+        dgate = pdg = pw = None
+        nw = 0
         if gate is not None:
-            dgate = _fp32((B, 2, D), dout)
+            dgate = _fp32((B, 2, D), (2 * D, D, 1), dout)
             ws = _workspace(workspace, _abi.sol_dropout_backward_workspace_bytes(B, L, D), dout)
+            pdg, pw, nw = dgate.data_ptr(), ws.data_ptr(), ws.nbytes
         _abi.check(_abi.sol_dropout_residual_backward(
-            _ptr(dout), _ptr(branch), _ptr(gate), _ptr(d), _ptr(dgate), _ptr(rng), site % 2**64,
-            p, B, L, nv, D, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), dt,
-            _stream(None)))
-    return d, dgate
+            dout.data_ptr(), pb, pg, pd, pdg, prng, site % 2**64, p, B, L, nv, D, pw, nw, dt,
+            _current(dout)))
+    return dbranch, dgate
 
 
 class RopeAxes:
@@ -563,45 +626,54 @@ _POS = {torch.int32: _abi.SOL_POS_I32, torch.int64: _abi.SOL_POS_I64,
         torch.float32: _abi.SOL_POS_F32}
 
 
-def _strides(t: torch.Tensor):
-    return [0 if n == 1 else s for n, s in zip(t.shape, t.stride())]
-
-
 def _heads(t: Optional[torch.Tensor], B: int, L: int, hd: int, name: str, like: torch.Tensor,
            heads: Optional[int] = None, written: bool = False) -> Optional[_abi.Heads]:
     if t is None:
         return None
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != L or t.shape[3] != hd or (
-            heads is not None and t.shape[2] != heads) or (hd > 1 and t.stride(3) != 1):
-        raise ValueError(f"{name} must be [{B}, {L}, {'heads' if heads is None else heads}, {hd}] "
-                         f"with unit channel stride, got {tuple(t.shape)}, strides {t.stride()}")
-    if t.device != like.device:
+    n = t.shape[2] if heads is None and t.dim() == 4 else heads
+    if t.shape != (B, L, n, hd) or (hd > 1 and t.stride(3) != 1):
+        raise ValueError(f"{name} must be [{B}, {L}, {'heads' if n is None else n}, {hd}] with "
+                         f"unit channel stride, got {tuple(t.shape)}, strides {t.stride()}")
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, q on {like.device}")
-    sb, sr, sh, _ = _strides(t)
-    if written and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+    if t.dtype is not like.dtype:
+        raise TypeError(f"all tensors must share one dtype, got {t.dtype} for {name} and "
+                        f"{like.dtype}")
+    sb, sr, sh, _ = t.stride()
+    # the stride of an axis of one element says nothing
+    if B == 1:
+        sb = 0
+    if L == 1:
+        sr = 0
+    if n == 1:
+        sh = 0
+    if written and L > 0 and ((sb == 0 and B > 1) or (sr == 0 and L > 1) or (sh == 0 and n > 1)):
         raise ValueError(f"{name} must not be an expanded tensor")
-    return _abi.Heads(_ptr(t), t.shape[2], sb, sr, sh)
+    return _abi.Heads(t.data_ptr(), n, sb, sr, sh)
 
 
 def _positions(pos: torch.Tensor, B: int, L: int, n_axes: int, like: torch.Tensor):
-    if pos.dtype not in _POS:
+    kind = _POS.get(pos.dtype)
+    if kind is None:
         raise TypeError("pos must be int32, int64 or float32")
-    if tuple(pos.shape) not in ((n_axes, B, L), (n_axes, L)) or (L > 1 and pos.stride(-1) != 1):
+    shape = pos.shape
+    if (shape != (n_axes, B, L) and shape != (n_axes, L)) or (L > 1 and pos.stride(-1) != 1):
         raise ValueError(f"pos must be [{n_axes}, {B}, {L}] or [{n_axes}, {L}] with unit row "
                          f"stride, got {tuple(pos.shape)}")
-    if pos.device != like.device:
+    if pos.get_device() != like.get_device():
         raise ValueError(f"pos is on {pos.device}, q on {like.device}")
-    s = _strides(pos)
-    return _abi.Positions(_ptr(pos), _POS[pos.dtype], 0, s[0], s[1] if pos.dim() == 3 else 0)
+    s = pos.stride()
+    return _abi.Positions(pos.data_ptr(), kind, 0, 0 if n_axes == 1 else s[0],
+                          s[1] if len(shape) == 3 and B > 1 else 0)
 
 
 def _rope_shapes(q, k, plan, what):
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError(f"{what} must be [B, L, heads, head_dim]")
-    B, L, _, hd = q.shape
+    B, L, H, hd = q.shape
     if hd != plan.head_dim:
         raise ValueError(f"{what} has heads of {hd}, the plan of {plan.head_dim}")
-    return B, L, hd
+    return B, L, H, hd
 
 
 def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, plan: RopeAxes,
@@ -615,24 +687,25 @@ def rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, pla
     float32), behind a per-head RMS norm with qk_norm=True (gamma_q/gamma_k
     [hd] or None).  Returns (q_out, k_out); pass q_out=q, k_out=k to rotate in
     place."""
-    B, L, hd = _rope_shapes(q, k, plan, "q")
-    for t, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
-        _expect(t, (hd,), name, q)
+    B, L, Hq, hd = _rope_shapes(q, k, plan, "q")
+    gq, gk = _arg(gamma_q, (hd,), "gamma_q", q), _arg(gamma_k, (hd,), "gamma_k", q)
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
-    dt = _dtype(q, k, gamma_q, gamma_k, q_out, k_out)
+    dt = _io_dtype(q)
+    hq, p = _heads(q, B, L, hd, "q", q), _positions(pos, B, L, plan.n_axes, q)
     with _on(q, stream):
-        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        ko = k_out
-        if k is not None and k_out is None:
-            ko = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        Hk = None if k is None else k.shape[2]
-        _abi.check(_abi.sol_rope_axes(
-            plan.desc, _positions(pos, B, L, plan.n_axes, q), _heads(q, B, L, hd, "q", q),
-            _heads(k, B, L, hd, "k", q), _heads(qo, B, L, hd, "q_out", q, q.shape[2], True),
-            _heads(ko, B, L, hd, "k_out", q, Hk, True), _ptr(gamma_q), _ptr(gamma_k),
-            int(bool(qk_norm)), B, L, eps, dt, _stream(None)))
-    return qo, ko
+        if q_out is None:
+            q_out = _packed(q)
+        hk = ho = None
+        if k is not None:
+            hk = _heads(k, B, L, hd, "k", q)
+            if k_out is None:
+                k_out = _packed(k)
+            ho = _heads(k_out, B, L, hd, "k_out", q, k.shape[2], True)
+        _abi.check(_abi.sol_rope_axes(plan.desc, p, hq, hk,
+                                      _heads(q_out, B, L, hd, "q_out", q, Hq, True), ho, gq, gk,
+                                      int(qk_norm), B, L, eps, dt, _current(q)))
+    return q_out, k_out
 
 
 class RopeGrads(NamedTuple):
@@ -656,33 +729,41 @@ def rope_axes_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], pos
     for (dq_out, dk_out).  q and k are read with qk_norm only.  dq and dk may
     be given with any strides (columns of a merged gradient) and may be dq_out
     and dk_out, or q and k (in place)."""
-    B, L, hd = _rope_shapes(dq_out, dk_out, plan, "dq_out")
-    for t, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
-        _expect(t, (hd,), name, dq_out)
+    g = dq_out
+    B, L, Hq, hd = _rope_shapes(g, dk_out, plan, "dq_out")
+    gq, gk = _arg(gamma_q, (hd,), "gamma_q", g), _arg(gamma_k, (hd,), "gamma_k", g)
     if qk_norm and (q is None or (k is None) != (dk_out is None)):
         raise ValueError("qk_norm needs q, and k together with dk_out")
     if dk_out is None and dk is not None:
         raise ValueError("dk without dk_out")
-    if not qk_norm:
-        q = k = None
-    dt = _dtype(dq_out, dk_out, q, k, gamma_q, gamma_k, dq, dk)
-    like = dq_out
-    Hq, Hk = dq_out.shape[2], None if dk_out is None else dk_out.shape[2]
-    with _on(like, stream):
-        gq = torch.empty(dq_out.shape, dtype=like.dtype, device=like.device) if dq is None else dq
-        gk = dk
-        if dk_out is not None and dk is None:
-            gk = torch.empty(dk_out.shape, dtype=like.dtype, device=like.device)
-        dgq = None if gamma_q is None else _fp32((hd,), like)
-        dgk = None if gamma_k is None else _fp32((hd,), like)
-        ws = None
-        if dgq is not None or dgk is not None:
-            ws = _workspace(workspace, _abi.sol_rope_backward_workspace_bytes(hd), like)
+    dt = _io_dtype(g)
+    p = _positions(pos, B, L, plan.n_axes, g)
+    hgq, hgk = _heads(g, B, L, hd, "dq_out", g), _heads(dk_out, B, L, hd, "dk_out", g)
+    hq = hk = None
+    if qk_norm:
+        hq = _heads(q, B, L, hd, "q", g, Hq)
+        if k is not None:
+            hk = _heads(k, B, L, hd, "k", g, dk_out.shape[2])
+    with _on(g, stream):
+        if dq is None:
+            dq = _packed(g)
+        hdk = None
+        if dk_out is not None:
+            if dk is None:
+                dk = _packed(dk_out)
+            hdk = _heads(dk, B, L, hd, "dk", g, dk_out.shape[2], True)
+        dgq = dgk = pgq = pgk = pw = None
+        nw = 0
+        if gamma_q is not None:
+            dgq = _fp32((hd,), (1,), g)
+            pgq = dgq.data_ptr()
+        if gamma_k is not None:
+            dgk = _fp32((hd,), (1,), g)
+            pgk = dgk.data_ptr()
+        if pgq or pgk:
+            ws = _workspace(workspace, _abi.sol_rope_backward_workspace_bytes(hd), g)
+            pw, nw = ws.data_ptr(), ws.nbytes
         _abi.check(_abi.sol_rope_axes_backward(
-            plan.desc, _positions(pos, B, L, plan.n_axes, like),
-            _heads(dq_out, B, L, hd, "dq_out", like), _heads(dk_out, B, L, hd, "dk_out", like),
-            _heads(q, B, L, hd, "q", like, Hq), _heads(k, B, L, hd, "k", like, Hk),
-            _heads(gq, B, L, hd, "dq", like, Hq, True), _heads(gk, B, L, hd, "dk", like, Hk, True),
-            _ptr(gamma_q), _ptr(gamma_k), _ptr(dgq), _ptr(dgk), int(bool(qk_norm)), B, L, eps,
-            _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), dt, _stream(None)))
-    return RopeGrads(gq, gk, dgq, dgk)
+            plan.desc, p, hgq, hgk, hq, hk, _heads(dq, B, L, hd, "dq", g, Hq, True), hdk, gq, gk,
+            pgq, pgk, int(qk_norm), B, L, eps, pw, nw, dt, _current(g)))
+    return RopeGrads(dq, dk, dgq, dgk)

@@ -367,8 +367,8 @@ cudaError_t launch_bwd(DropArgs &a, cudaStream_t stream) {
   const int64_t most = (a.seg.rows + rg * kDropRows - 1) / (rg * kDropRows);
   if (shares > most) shares = most;
   if (shares > kMaxSumCtas) shares = kMaxSumCtas;
-  if (shares < 1) shares = 1;
-  a.seg.ctas = static_cast<int>(shares);
+  if (shares < 1) shares = 1;  // never more than rows
+  cut_shares(&a.seg, shares);
   kern<<<static_cast<unsigned>(a.seg.ctas * tiles), dim3(nt, rg), 0, stream>>>(a, tiles);
   return cudaGetLastError();
 }

@@ -41,7 +41,7 @@ __device__ __forceinline__ uint4 ld_staged(const uint4 *p) {
 // registers) and 0.78 ms at 96 registers, which spill.
 constexpr int kLnThreadsPerSm = 512;
 
-template <typename T, int NT, int VPT, int R, int S, int K>
+template <typename T, int NT, int VPT, int R, int S, int K, bool FULL>
 __global__ void __launch_bounds__(NT, kLnThreadsPerSm / NT < 16 ? kLnThreadsPerSm / NT : 16)
     layer_norm_kernel(const LnArgs a) {
   static_assert(K % R == 0, "an iteration's rows must lie in one chunk");
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(NT, kLnThreadsPerSm / NT < 16 ? kLnThreadsPerS
 
   bool ok[VPT];
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) ok[k] = k * NT + tid < a.nvec;
+  for (int k = 0; k < VPT; ++k) ok[k] = FULL || k * NT + tid < a.nvec;
   // elements of a row that this warp holds
   float n_w = 0.f;
 #pragma unroll
@@ -282,10 +282,10 @@ constexpr int kLnRows = VPT <= 5 ? 2 : 1;
 // chunk of consecutive rows per CTA turn, as RMS-AdaLN's
 constexpr int kLnChunk = 8;
 
-template <typename T, int NT, int VPT>
+template <typename T, int NT, int VPT, bool FULL>
 cudaError_t launch_t(const LnArgs &a, cudaStream_t stream) {
   constexpr int R = kLnRows<VPT>, S = 2;
-  auto *kern = &layer_norm_kernel<T, NT, VPT, R, S, kLnChunk>;
+  auto *kern = &layer_norm_kernel<T, NT, VPT, R, S, kLnChunk, FULL>;
   const void *fn = reinterpret_cast<const void *>(kern);
   const size_t smem = 2 * R * (NT / 32) * 16 + static_cast<size_t>(S) * R * VPT * NT * 16;
   const int per_sm = resident_blocks(fn, NT, smem);
@@ -296,10 +296,18 @@ cudaError_t launch_t(const LnArgs &a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// A short launch whose split covers the row exactly takes the unguarded
+// instantiation (FULL), as in RMS-AdaLN: 36.7 against 41.0 us at 8,264 rows of
+// 5120 bf16; at 126,552 rows it was 3% slower.
+constexpr int64_t kFullMaxRows = 16384;
+
 template <typename T>
 cudaError_t dispatch(const LnArgs &a, int threads, int vpt, cudaStream_t stream) {
-#define SOL_CASE(NT, V) \
-  if (threads == NT && vpt == V) return launch_t<T, NT, V>(a, stream);
+#define SOL_CASE(NT, V)                                       \
+  if (threads == NT && vpt == V)                              \
+    return a.nvec == NT * V && a.rows <= kFullMaxRows        \
+               ? launch_t<T, NT, V, true>(a, stream)          \
+               : launch_t<T, NT, V, false>(a, stream);
   SOL_SPLITS(SOL_CASE)
 #undef SOL_CASE
   return cudaErrorInvalidValue;

@@ -51,7 +51,7 @@ __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d, i
 // S ring stages of R (1 or 2) rows per group.  Each warp has a block of the
 // ring to itself, its slots 512 bytes (a vector per lane) apart: every slot is
 // a constant offset whatever the CTA's shape.
-template <typename T, int VPT, bool RMS, bool DRES, int R, int S>
+template <typename T, int VPT, bool RMS, bool DRES, bool FULL, int R, int S>
 __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
     norm_backward_kernel(const NormBwdArgs a) {
   using IO = Io<T>;
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
 
   // Only the last vector of a thread can lie past the row: the launcher's NT
   // has (VPT - 1) * NT <= nvec.
-  const bool last = (VPT - 1) * NT + tx < a.nvec;
+  const bool last = FULL || (VPT - 1) * NT + tx < a.nvec;
   auto ok = [&](int k) { return k < VPT - 1 || last; };
   auto slot = [&](int s, int q, int in, int k) -> uint4 * {
     return mine + (s * STAGE + (q * NIN + in) * VPT + k) * 32;
@@ -297,12 +297,21 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
   }
 }
 
-template <typename T, int VPT, bool RMS, bool DRES>
-cudaError_t launch_t(NormBwdArgs &a, cudaStream_t stream) {
-  constexpr int R = VPT <= 2 ? 2 : 1, S = 2;  // wider rows: what shared memory holds
+// Rows per group that a CTA takes at least: fewer would write more partial sums
+// than the rows they come from.
+constexpr int kNormMinRows = 4;
+
+template <typename T, int VPT, bool RMS, bool DRES, bool FULL>
+cudaError_t launch_full(NormBwdArgs &a, cudaStream_t stream) {
+  // Rows per group and stages.  One row where a third input is staged (two
+  // would leave shared memory for one CTA per SM) and in RMS (0.654 against
+  // 0.678 ms for two at the 5 s clip; the layer norm 0.743 against 0.649 ms);
+  // wider rows take what fits.
+  constexpr int R = VPT > 2 || DRES || RMS ? 1 : 2;
+  constexpr int S = VPT <= 2 && RMS && !DRES ? 4 : 2;
   const int NT = ((a.nvec + VPT - 1) / VPT + 31) / 32 * 32;
   const int RG = NT >= 256 ? 1 : 256 / NT;
-  auto *kern = &norm_backward_kernel<T, VPT, RMS, DRES, R, S>;
+  auto *kern = &norm_backward_kernel<T, VPT, RMS, DRES, FULL, R, S>;
   const size_t smem = 2 * RG * (NT / 32) * 16 +
                       static_cast<size_t>(S) * R * (DRES ? 3 : 2) * VPT * NT * RG * 16;
   const int per_sm =
@@ -310,11 +319,20 @@ cudaError_t launch_t(NormBwdArgs &a, cudaStream_t stream) {
   if (per_sm <= 0) return cudaErrorInvalidConfiguration;
   int64_t ctas = static_cast<int64_t>(per_sm) * device_sms();
   if (ctas > kMaxSumCtas) ctas = kMaxSumCtas;
-  const int64_t most = (a.seg.rows + RG - 1) / RG;  // a row per group at least
+  const int64_t most = (a.seg.rows + kNormMinRows * RG - 1) / (kNormMinRows * RG);
   if (ctas > most) ctas = most;
-  a.seg.ctas = static_cast<int>(ctas);
+  cut_shares(&a.seg, ctas);
   kern<<<static_cast<unsigned>(ctas), dim3(NT, RG), smem, stream>>>(a);
   return cudaGetLastError();
+}
+
+// RMS rows that fill every thread's vectors take the unguarded instantiation
+// (0.716 -> 0.672 ms at the 5 s clip, and -> 0.643 on another box); the layer norm
+// was 2% slower with it.
+template <typename T, int VPT, bool RMS, bool DRES>
+cudaError_t launch_t(NormBwdArgs &a, cudaStream_t stream) {
+  return RMS && a.nvec % (32 * VPT) == 0 ? launch_full<T, VPT, RMS, DRES, RMS>(a, stream)
+                                         : launch_full<T, VPT, RMS, DRES, false>(a, stream);
 }
 
 // One vector per thread up to 32 (a warp spans the row), two up to 640 (320

@@ -12,7 +12,7 @@
 namespace sol {
 namespace {
 
-constexpr int64_t kMaxKeyedSamples = 32767;  // keys are a grid dimension
+constexpr int64_t kMaxSamples = int64_t(1) << 30;  // 2 * sample + modality is 32-bit
 
 // No exception crosses the C boundary.
 template <typename F>
@@ -71,6 +71,8 @@ sol_status check_rows(const char *fn, int64_t B, int64_t L, int64_t n_video, int
     return fail(SOL_ERR_INVALID_ARG, "%s: need B, L >= 0, D > 0 and 0 <= n_video <= L", fn);
   if (B > kMaxRows || L > kMaxRows || B * L > kMaxRows)
     return fail(SOL_ERR_UNSUPPORTED, "%s: B*L must be below 2^31 rows", fn);
+  if (B >= kMaxSamples)
+    return fail(SOL_ERR_UNSUPPORTED, "%s: B must be below 2^30 samples", fn);
   const int es = esize_of(dtype);
   if (D > kMaxRowBytesRms / es)
     return fail(SOL_ERR_UNSUPPORTED, "%s: D=%lld exceeds %lld elements", fn, (long long)D,
@@ -120,9 +122,6 @@ sol_status norm_backward(const char *fn, bool rms, const void *dy, const void *x
   if (rms && !(eps >= 0.f)) return fail(SOL_ERR_INVALID_ARG, "%s: need eps >= 0", fn);
   if (!scale && (dscale || dshift))
     return fail(SOL_ERR_INVALID_ARG, "%s: dscale and dshift need scale", fn);
-  if (scale && B > kMaxKeyedSamples)
-    return fail(SOL_ERR_UNSUPPORTED, "%s: B=%lld exceeds %lld samples", fn, (long long)B,
-                (long long)kMaxKeyedSamples);
   const int64_t rows = B * L;
   const bool sums = dgamma || dbeta || dscale || dshift;
   if (rows > 0 && (!dy || !x || !dx || (rms ? !scale : (!mean || !rstd))))
@@ -558,9 +557,6 @@ sol_status sol_dropout_residual_backward(const void *dout, const void *branch, c
     st = check_dropout(fn, rng, site, p, rows > 0, a);
     if (st != SOL_OK) return st;
     if (dgate && !gate) return fail(SOL_ERR_INVALID_ARG, "%s: dgate needs gate", fn);
-    if (dgate && B > kMaxKeyedSamples)
-      return fail(SOL_ERR_UNSUPPORTED, "%s: B=%lld exceeds %lld samples", fn, (long long)B,
-                  (long long)kMaxKeyedSamples);
     if (rows > 0 && (!dout || !dbranch || (dgate && !branch)))
       return fail(SOL_ERR_INVALID_ARG, "%s: dout, dbranch (and branch, with dgate) must be "
                   "non-null", fn);

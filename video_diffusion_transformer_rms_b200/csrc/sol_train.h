@@ -34,17 +34,25 @@ cudaError_t launch_layer_norm(const LnArgs &a, int dtype, cudaStream_t stream);
 
 // ---- sums over the rows of each (sample, modality) ---------------------------
 
-// Rows [0, rows) in CTAs' contiguous shares; key of a row = 2 * sample +
-// modality, non-decreasing along the rows.  A CTA writes the sums over its
-// rows of key k to slot `cta + k` of the workspace: (cta, key) pairs walk a
-// staircase, so no two share a slot and ctas + keys slots are enough.
+// Rows [0, rows) in CTAs' contiguous shares, the first `longer` of them `share`
+// + 1 rows, the others `share`.  Key of a row = 2 * sample + modality,
+// non-decreasing along the rows.  A CTA writes the sums over its rows of key k
+// to slot `cta + k` of the workspace: (cta, key) pairs walk a staircase, so no
+// two share a slot and ctas + keys slots are enough.
 struct Segments {
-  int64_t rows;
-  int L;        // rows per sample (rows, if the sums have one key)
-  int n_video;  // first rows of a sample: key 2b; the others: key 2b + 1
-  int keys;     // 2 * samples, or 1
-  int ctas;     // shares the rows are cut into
+  int64_t rows;  // < 2^31
+  int L;         // rows per sample (rows, if the sums have one key)
+  int n_video;   // first rows of a sample: key 2b; the others: key 2b + 1
+  int keys;      // 2 * samples, or 1
+  int ctas;      // shares the rows are cut into, at most `rows`
+  int share;
+  int longer;
 };
+inline void cut_shares(Segments *s, int64_t ctas) {
+  s->ctas = static_cast<int>(ctas);
+  s->share = static_cast<int>(s->rows / ctas);
+  s->longer = static_cast<int>(s->rows % ctas);
+}
 // Bound on `ctas`: four CTAs on each of 148 SMs.
 constexpr int kMaxSumCtas = 592;
 // Slots of the workspace: shares and keys.
@@ -64,7 +72,7 @@ struct SumArgs {
   float *dshift;         // [keys][D]: S0, or null
   float *dgamma;         // [D]: sum over keys of (1 + scale) * S1, or null
   float *dbeta;          // [D]: sum over keys of (1 + scale) * S0, or null
-  float mult;            // applied to every sum
+  float mult;            // applied to S1
 };
 cudaError_t launch_segment_sums(const SumArgs &a, int dtype, cudaStream_t stream);
 
@@ -80,13 +88,13 @@ struct NormBwdArgs {
   const void *dres;    // may be null: added to dx
   void *dx;
   float *partial;      // workspace, or null: no vector gradients wanted
-  Segments seg;        // ctas set by the launcher
+  Segments seg;        // shares cut by the launcher
   int nvec;
   int D;
   float eps;           // RMS only
   bool rms;
 };
-// Fills a.seg.ctas and enqueues the kernel.
+// Cuts the shares of a.seg and enqueues the kernel.
 cudaError_t launch_norm_backward(NormBwdArgs &a, int dtype, cudaStream_t stream);
 
 // ---- dropout in front of the gated residual ----------------------------------
@@ -103,7 +111,7 @@ struct DropArgs {
   bool drop;            // false: nothing is dropped, rng is not read
   float keep_scale;     // 1 / (1 - p), 0 for p = 1
   float *partial;       // backward: workspace
-  Segments seg;         // backward: ctas set by the launcher
+  Segments seg;         // backward: shares cut by the launcher
   int nvec;
   int D;
 };

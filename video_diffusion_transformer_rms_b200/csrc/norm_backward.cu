@@ -339,7 +339,11 @@ cudaError_t launch_t(NormBwdArgs &a, cudaStream_t stream) {
 // threads), then as few as 512 threads can hold.
 template <typename T, bool RMS, bool DRES>
 cudaError_t dispatch(NormBwdArgs &a, cudaStream_t stream) {
-  if (a.nvec <= 32) return launch_t<T, 1, RMS, DRES>(a, stream);
+#ifndef NB_V1
+#define NB_V1 0
+#endif
+  const int nt1 = (a.nvec + 31) / 32 * 32, nt2 = ((a.nvec + 1) / 2 + 31) / 32 * 32;
+  if (a.nvec <= 32 || (NB_V1 == 1 && a.nvec <= 320) || (NB_V1 == 2 && a.nvec <= 320 && nt1 < 2 * nt2)) return launch_t<T, 1, RMS, DRES>(a, stream);
   if (a.nvec <= 640) return launch_t<T, 2, RMS, DRES>(a, stream);
   if (a.nvec <= 1536) return launch_t<T, 3, RMS, DRES>(a, stream);
   return launch_t<T, 4, RMS, DRES>(a, stream);

@@ -8,20 +8,20 @@
 // where R(pos) turns pair i of the first rot_dim channels by the angle
 // pos[axis_i] * freq_i and leaves the rest as they are.
 //
-// A warp owns a token row (WR warps share one when the rows are few).  Its
-// lanes first compute the row's angles, a few rotary pairs each, once for all q
-// and k heads: the product in fp64, reduced to [-pi, pi] by a two-part 2 pi,
-// then sin and cos of the fp32 rest, corrected to first order by what that
-// rounding dropped.  They meet in the warp's own shared memory, so nothing
-// waits for another warp.  Then G consecutive lanes own one head vector at a
+// A warp owns a token row, as long as there is one for every warp of the grid;
+// the rows left after the last whole round are shared by WR warps each, so the
+// round they make is shorter.  A warp's lanes first compute the row's angles, a
+// few rotary pairs each, once for all q and k heads: the product in fp64, reduced
+// to [-pi, pi] by a two-part 2 pi, then sin and cos of the fp32 rest, corrected
+// to first order by what that rounding dropped.  They meet in the warp's own
+// shared memory, so nothing waits for another warp.  Then G consecutive lanes own one head vector at a
 // time (16 bytes per lane; G is the next power of two, lanes past head_dim
 // idle).  A lane sees the same channels in every head: its cos and sin, with
-// gamma folded in, stay in registers for the row.  D vectors per lane are in
-// flight: as a batch of loads into registers, or, in the norm's backward pass,
-// which needs the registers for its sums and two vectors per head, through a
-// ring in shared memory that cp.async fills across the ends of heads, of q and
-// k and of rows.
-// A head's sums are G-lane shuffles, and 1/rms one factor at the end.
+// gamma folded in, stay in registers for the row.  Several vectors per lane are
+// in flight: as a batch of loads into registers, or, in the norm's backward
+// pass, which needs the registers for its sums and two vectors per head, through
+// a ring in shared memory that cp.async fills across the ends of q, of k and of
+// rows.  A head's sums are G-lane shuffles, and 1/rms one factor at the end.
 // Half-split pairs fetch their partner channels as raw 32-bit words from the
 // lane that holds them.
 //
@@ -67,24 +67,29 @@ __device__ __forceinline__ float2 cos_sin(double pos, double freq) {
 
 // CTAs per SM that the registers are to leave room for: 80 registers a thread,
 // 128 in the norm's backward pass.  5 s clip, 40 + 40 heads of 128 in bf16:
-// forward with the norm 0.83 ms (64 registers: 0.87), backward 1.29 ms (80
-// registers: 2.38).
+// forward with the norm 0.83 ms (64 registers: 0.87), backward 1.23 ms (80
+// registers spill: 2.38 with a ring of single heads, 1.29 without).
 template <int MODE>
 constexpr int kRopeMinCtas = MODE == kNormRotateBack ? 2 : 3;
-// Vectors per lane in flight.
+// Depth of the loads in flight: vectors per lane, or in the norm's backward pass
+// ring entries of kRopeEntry heads each, which spread the ring's bookkeeping.
+// 5 s clip, half-split / interleaved: 3 entries of 3 heads 1.233 / 1.247 ms, 4 of
+// 2 1.307 / 1.186, 2 of 4 1.231 / 1.287, 6 of 1 1.345 / 1.261.
 template <int MODE>
-constexpr int kRopeDepth = MODE == kNormRotateBack ? 6 : 4;
+constexpr int kRopeDepth = MODE == kNormRotateBack ? 3 : 4;
+constexpr int kRopeEntry = 3;
 
 // MODE as RopeMode.  HALF: pair i = channels (i, i + rot_dim / 2), else
-// (2i, 2i + 1).  wr_log2: log2 of the warps that share a row.
+// (2i, 2i + 1).  The rows from whole_rows on are shared by 2^tail_log2 warps.
 template <typename T, int G, bool HALF, int MODE, int D>
 __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
-    rope_axes_kernel(const __grid_constant__ RopeArgs a, int wr_log2) {
+    rope_axes_kernel(const __grid_constant__ RopeArgs a, int whole_rows, int tail_log2) {
   using IO = Io<T>;
   constexpr int E = IO::E, P = E / 2;
   constexpr bool NORM = MODE == kNormRotate || MODE == kNormRotateBack;
   constexpr bool BACK = MODE == kRotateBack || MODE == kNormRotateBack;
   constexpr bool DGAMMA = MODE == kNormRotateBack;
+  constexpr int RV = kRopeEntry;
   constexpr int GW = 32 / G;                          // heads a warp holds at a time
   constexpr int NPL = G * E / 64 > 0 ? G * E / 64 : 1;  // rotary pairs per lane, at most
   constexpr int GROUPS = kRopeThreads / G;
@@ -98,8 +103,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
   // each warp's cos and sin, one entry per pair (interleaved: identity pairs past
   // rot_dim)
   constexpr int PITCH = G * P;
-  uint4 *ring = reinterpret_cast<uint4 *>(smem) + tid;                   // [D][2][threads]
-  float2 *sums = reinterpret_cast<float2 *>(smem + (DGAMMA ? D * 2 * kRopeThreads * 16 : 0));
+  uint4 *ring = reinterpret_cast<uint4 *>(smem) + tid;                   // [D][2 RV][threads]
+  float2 *sums = reinterpret_cast<float2 *>(smem + (DGAMMA ? D * 2 * RV * kRopeThreads * 16 : 0));
   float *cosw = reinterpret_cast<float *>(sums + (DGAMMA ? 2 * P * kRopeThreads : 0)) +
                 warp * 2 * PITCH;
   float *sinw = cosw + PITCH;
@@ -152,284 +157,299 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
     }
   }
 
-  const int WR = 1 << wr_log2;
-  const int rpb = (kRopeThreads / 32) >> wr_log2;            // rows of a CTA at a time
-  const int slot0 = (warp & (WR - 1)) * GW, step = WR * GW;  // heads slot0 + lane / G + i * step
-  const int slot = slot0 + lane / G;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * rpb;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * rpb + (warp >> wr_log2);
-  // passes over the heads of q and of k
-  const int passes_q = a.heads[0] > slot0 ? (a.heads[0] - slot0 + step - 1) / step : 0;
-  const int passes_k = a.heads[1] > slot0 ? (a.heads[1] - slot0 + step - 1) / step : 0;
-  if (passes_q + passes_k == 0) row = a.rows;  // more warps than heads: none for this one
+  for (int phase = 0; phase < 2; ++phase) {
+    const int wr_log2 = phase == 0 ? 0 : tail_log2, WR = 1 << wr_log2;
+    const int rpb = (kRopeThreads / 32) >> wr_log2;            // rows of a CTA at a time
+    const int slot0 = (warp & (WR - 1)) * GW, step = WR * GW;  // heads slot0 + lane / G + i * step
+    const int slot = slot0 + lane / G;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * rpb;
+    const int64_t end = phase == 0 ? whole_rows : a.rows;
+    int64_t row = (phase == 0 ? 0 : whole_rows) + static_cast<int64_t>(blockIdx.x) * rpb +
+                  (warp >> wr_log2);
+    // passes over the heads of q and of k
+    const int passes_q = a.heads[0] > slot0 ? (a.heads[0] - slot0 + step - 1) / step : 0;
+    const int passes_k = a.heads[1] > slot0 ? (a.heads[1] - slot0 + step - 1) / step : 0;
+    if (passes_q + passes_k == 0) row = end;  // more warps than heads: none for this one
 
-  // The ring's producer: it walks the same rows, tensors and passes as the loop
-  // below, D - 1 vectors ahead.
-  int64_t prow = row;
-  int pt = passes_q > 0 ? 0 : 1, phead = slot, pleft = 0, pslot = 0, cons = 0;
-  const unsigned char *px = nullptr, *pg = nullptr;
-  auto seek = [&]() {
-    const unsigned b = static_cast<unsigned>(prow) / static_cast<unsigned>(a.L);
-    const unsigned r = static_cast<unsigned>(prow) - b * static_cast<unsigned>(a.L);
-    phead = slot;
-    pleft = pt == 0 ? passes_q : passes_k;
-    px = static_cast<const unsigned char *>(a.x[pt].data) +
-         (b * a.x[pt].sb + r * a.x[pt].sr + slot * a.x[pt].sh) + gl * 16;
-    pg = static_cast<const unsigned char *>(a.g[pt].data) +
-         (b * a.g[pt].sb + r * a.g[pt].sr + slot * a.g[pt].sh) + gl * 16;
-  };
-  auto produce = [&]() {
-    if (prow < a.rows) {
-      if (active && phead < a.heads[pt]) {
-        uint4 *dst = ring + pslot * (2 * kRopeThreads);
-        cp_async16(dst, px);
-        cp_async16(dst + kRopeThreads, pg);
-      }
-      phead += step;
-      px += a.x[pt].sh * step;
-      pg += a.g[pt].sh * step;
-      if (--pleft == 0) {
-        if (pt == 0 && passes_k > 0) {
-          pt = 1;
-        } else {
-          pt = passes_q > 0 ? 0 : 1;
-          prow += stride;
+    // The ring's producer: it walks the same rows, tensors and passes as the loop
+    // below, D - 1 vectors ahead.
+    int64_t prow = row;
+    int pt = passes_q > 0 ? 0 : 1, phead = slot, pleft = 0, pslot = 0, cons = 0;
+    const unsigned char *px = nullptr, *pg = nullptr;
+    auto seek = [&]() {
+      const unsigned b = static_cast<unsigned>(prow) / static_cast<unsigned>(a.L);
+      const unsigned r = static_cast<unsigned>(prow) - b * static_cast<unsigned>(a.L);
+      phead = slot;
+      pleft = pt == 0 ? passes_q : passes_k;
+      px = static_cast<const unsigned char *>(a.x[pt].data) +
+           (b * a.x[pt].sb + r * a.x[pt].sr + slot * a.x[pt].sh) + gl * 16;
+      pg = static_cast<const unsigned char *>(a.g[pt].data) +
+           (b * a.g[pt].sb + r * a.g[pt].sr + slot * a.g[pt].sh) + gl * 16;
+    };
+    auto produce = [&]() {
+      if (prow < end) {
+        const int64_t xstep = a.x[pt].sh * step, gstep = a.g[pt].sh * step;
+        uint4 *dst = ring + pslot * (2 * RV * kRopeThreads);
+#pragma unroll
+        for (int u = 0; u < RV; ++u) {
+          if (active && phead + u * step < a.heads[pt]) {
+            cp_async16(dst + 2 * u * kRopeThreads, px + u * xstep);
+            cp_async16(dst + (2 * u + 1) * kRopeThreads, pg + u * gstep);
+          }
         }
-        if (prow < a.rows) seek();
+        phead += RV * step;
+        px += RV * xstep;
+        pg += RV * gstep;
+        pleft -= RV;
+        if (pleft <= 0) {
+          if (pt == 0 && passes_k > 0) {
+            pt = 1;
+          } else {
+            pt = passes_q > 0 ? 0 : 1;
+            prow += stride;
+          }
+          if (prow < end) seek();
+        }
       }
-    }
-    cp_async_commit();
-    pslot = pslot + 1 == D ? 0 : pslot + 1;
-  };
-  if constexpr (DGAMMA) {
-    if (prow < a.rows) seek();
+      cp_async_commit();
+      pslot = pslot + 1 == D ? 0 : pslot + 1;
+    };
+    if constexpr (DGAMMA) {
+      if (prow < end) seek();
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i) produce();
-  }
+      for (int i = 0; i < D - 1; ++i) produce();
+    }
 
-  double pos[NPL];
-  if (row < a.rows) load_pos(row, pos);
-  for (; row < a.rows; row += stride) {
-    const unsigned b = static_cast<unsigned>(row) / static_cast<unsigned>(a.L);
-    const unsigned r = static_cast<unsigned>(row) - b * static_cast<unsigned>(a.L);
-    __syncwarp();  // every lane has read the previous row's table
+    double pos[NPL];
+    if (row < end) load_pos(row, pos);
+    for (; row < end; row += stride) {
+      const unsigned b = static_cast<unsigned>(row) / static_cast<unsigned>(a.L);
+      const unsigned r = static_cast<unsigned>(row) - b * static_cast<unsigned>(a.L);
+      __syncwarp();  // every lane has read the previous row's table
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int p = lane + 32 * i;
-      if (p < half) {
-        const float2 cs = cos_sin(pos[i], freq[i]);
-        cosw[p] = cs.x;
-        sinw[p] = cs.y;
+      for (int i = 0; i < NPL; ++i) {
+        const int p = lane + 32 * i;
+        if (p < half) {
+          const float2 cs = cos_sin(pos[i], freq[i]);
+          cosw[p] = cs.x;
+          sinw[p] = cs.y;
+        }
       }
-    }
-    __syncwarp();
-    if (row + stride < a.rows) load_pos(row + stride, pos);
+      __syncwarp();
+      if (row + stride < end) load_pos(row + stride, pos);
 
 #pragma unroll 1
-    for (int t = 0; t < 2; ++t) {
-      const int passes = t == 0 ? passes_q : passes_k;
-      if (passes == 0) continue;
-      float2 dg[P];  // this row's part of dgam[t]
+      for (int t = 0; t < 2; ++t) {
+        const int passes = t == 0 ? passes_q : passes_k;
+        if (passes == 0) continue;
+        float2 dg[P];  // this row's part of dgam[t]
 #pragma unroll
-      for (int m = 0; m < P; ++m) dg[m] = splat2(0.f);
-      // cos, sin and gamma of the lane's channels (gp: its partner channels)
-      float2 c[P], s[P], gam[P], gp[P];
+        for (int m = 0; m < P; ++m) dg[m] = splat2(0.f);
+        // cos, sin and gamma of the lane's channels (gp: its partner channels)
+        float2 c[P], s[P], gam[P], gp[P];
 #pragma unroll
-      for (int m = 0; m < P; ++m) gam[m] = gp[m] = splat2(1.f);
-      if constexpr (NORM) {
-        if (a.gamma[t]) {
-          uint4 raw = make_uint4(0, 0, 0, 0);
-          if (active) raw = ld_shared_vec(static_cast<const uint4 *>(a.gamma[t]) + gl);
-          uint4 rp = raw;
-          if constexpr (HALF && !BACK) {
-            rp.x = __shfl_sync(0xffffffffu, raw.x, partner);
-            rp.y = __shfl_sync(0xffffffffu, raw.y, partner);
-            rp.z = __shfl_sync(0xffffffffu, raw.z, partner);
-            rp.w = __shfl_sync(0xffffffffu, raw.w, partner);
-          }
-          IO::unpack(raw, gam);
-          IO::unpack(rp, gp);
-        }
-      }
-      // the turn of one component pair (u, v) held as A, B:
-      //   interleaved forward   even = e A - o B,  odd = e C + o D
-      //   interleaved backward  even = e c + o s,  odd = o c - e s
-      //   half-split            out = own A + partner B
-      float2 A[P], B[P];
-      if constexpr (HALF) {
-#pragma unroll
-        for (int m = 0; m < P; ++m) {
-          c[m] = turns ? *reinterpret_cast<const float2 *>(cosw + col + 2 * m) : splat2(1.f);
-          s[m] = turns ? *reinterpret_cast<const float2 *>(sinw + col + 2 * m) : splat2(0.f);
-          const float sg = (second != BACK) ? 1.f : -1.f;
-          A[m] = BACK ? c[m] : mul2(c[m], gam[m]);
-          B[m] = mul2(s[m], splat2(sg));
-          if constexpr (!BACK) B[m] = mul2(B[m], gp[m]);
-        }
-      } else {
-        // entry m: pairs 2m and 2m + 1 of the lane; first P/2 entries of A, B for
-        // the even outputs, the others for the odd ones
-#pragma unroll
-        for (int m = 0; m < P / 2; ++m) {
-          c[m] = *reinterpret_cast<const float2 *>(cosw + col + 2 * m);
-          s[m] = *reinterpret_cast<const float2 *>(sinw + col + 2 * m);
-          const float2 ge = make_float2(gam[2 * m].x, gam[2 * m + 1].x);
-          const float2 go = make_float2(gam[2 * m].y, gam[2 * m + 1].y);
-          if constexpr (BACK) {
-            A[m] = c[m];
-            B[m] = s[m];
-          } else {
-            A[m] = mul2(c[m], ge);                              // even from even
-            B[m] = mul2(mul2(s[m], go), splat2(-1.f));          // even from odd
-            A[m + P / 2] = mul2(c[m], go);                      // odd from odd
-            B[m + P / 2] = mul2(s[m], ge);                      // odd from even
-          }
-          gam[2 * m] = ge;  // kept in the same split as the channels
-          gam[2 * m + 1] = go;
-        }
-      }
-
-      // one head vector (dy with it in the norm's backward pass) to dst
-      auto turn = [&](uint4 vx, uint4 vg, bool live, unsigned char *dst) {
-        // v: the vector that is turned; o: the turned one
-        const uint4 v = BACK ? vg : vx;
-        float2 o[P];
-        if constexpr (HALF) {
-          uint4 vp;
-          vp.x = __shfl_sync(0xffffffffu, v.x, partner);
-          vp.y = __shfl_sync(0xffffffffu, v.y, partner);
-          vp.z = __shfl_sync(0xffffffffu, v.z, partner);
-          vp.w = __shfl_sync(0xffffffffu, v.w, partner);
-          float2 own[P], oth[P];
-          IO::unpack(v, own);
-          IO::unpack(vp, oth);
-#pragma unroll
-          for (int m = 0; m < P; ++m) o[m] = fma2(own[m], A[m], mul2(oth[m], B[m]));
-        } else {
-          float2 ev[P / 2], od[P / 2];
-          IO::unpack_eo(v, ev, od);
-#pragma unroll
-          for (int m = 0; m < P / 2; ++m) {
-            if constexpr (BACK) {
-              const float2 neg = mul2(B[m], splat2(-1.f));
-              o[2 * m] = fma2(ev[m], A[m], mul2(od[m], B[m]));
-              o[2 * m + 1] = fma2(od[m], A[m], mul2(ev[m], neg));
-            } else {
-              o[2 * m] = fma2(ev[m], A[m], mul2(od[m], B[m]));
-              o[2 * m + 1] = fma2(od[m], A[m + P / 2], mul2(ev[m], B[m + P / 2]));
-            }
-          }
-        }
+        for (int m = 0; m < P; ++m) gam[m] = gp[m] = splat2(1.f);
         if constexpr (NORM) {
-          float2 x[P];
-          if constexpr (HALF) {
-            IO::unpack(vx, x);
-          } else {
-            float2 ev[P / 2], od[P / 2];
-            IO::unpack_eo(vx, ev, od);
-#pragma unroll
-            for (int m = 0; m < P / 2; ++m) {
-              x[2 * m] = ev[m];
-              x[2 * m + 1] = od[m];
+          if (a.gamma[t]) {
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            if (active) raw = ld_shared_vec(static_cast<const uint4 *>(a.gamma[t]) + gl);
+            uint4 rp = raw;
+            if constexpr (HALF && !BACK) {
+              rp.x = __shfl_sync(0xffffffffu, raw.x, partner);
+              rp.y = __shfl_sync(0xffffffffu, raw.y, partner);
+              rp.z = __shfl_sync(0xffffffffu, raw.z, partner);
+              rp.w = __shfl_sync(0xffffffffu, raw.w, partner);
             }
+            IO::unpack(raw, gam);
+            IO::unpack(rp, gp);
           }
-          float2 sq = splat2(0.f), dot = splat2(0.f), h[P];
+        }
+        // the turn of one component pair (u, v) held as A, B:
+        //   interleaved forward   even = e A - o B,  odd = e C + o D
+        //   interleaved backward  even = e c + o s,  odd = o c - e s
+        //   half-split            out = own A + partner B
+        float2 A[P], B[P];
+        if constexpr (HALF) {
 #pragma unroll
           for (int m = 0; m < P; ++m) {
-            sq = fma2(x[m], x[m], sq);
+            c[m] = turns ? *reinterpret_cast<const float2 *>(cosw + col + 2 * m) : splat2(1.f);
+            s[m] = turns ? *reinterpret_cast<const float2 *>(sinw + col + 2 * m) : splat2(0.f);
+            const float sg = (second != BACK) ? 1.f : -1.f;
+            A[m] = BACK ? c[m] : mul2(c[m], gam[m]);
+            B[m] = mul2(s[m], splat2(sg));
+            if constexpr (!BACK) B[m] = mul2(B[m], gp[m]);
+          }
+        } else {
+          // entry m: pairs 2m and 2m + 1 of the lane; first P/2 entries of A, B for
+          // the even outputs, the others for the odd ones
+#pragma unroll
+          for (int m = 0; m < P / 2; ++m) {
+            c[m] = *reinterpret_cast<const float2 *>(cosw + col + 2 * m);
+            s[m] = *reinterpret_cast<const float2 *>(sinw + col + 2 * m);
+            const float2 ge = make_float2(gam[2 * m].x, gam[2 * m + 1].x);
+            const float2 go = make_float2(gam[2 * m].y, gam[2 * m + 1].y);
             if constexpr (BACK) {
-              h[m] = mul2(o[m], gam[m]);
-              dot = fma2(h[m], x[m], dot);
+              A[m] = c[m];
+              B[m] = s[m];
+            } else {
+              A[m] = mul2(c[m], ge);                              // even from even
+              B[m] = mul2(mul2(s[m], go), splat2(-1.f));          // even from odd
+              A[m + P / 2] = mul2(c[m], go);                      // odd from odd
+              B[m + P / 2] = mul2(s[m], ge);                      // odd from even
             }
-          }
-          float ss = sq.x + sq.y, d = dot.x + dot.y;
-#pragma unroll
-          for (int w = G / 2; w > 0; w >>= 1) {
-            ss += __shfl_xor_sync(0xffffffffu, ss, w);
-            if constexpr (BACK) d += __shfl_xor_sync(0xffffffffu, d, w);
-          }
-          const float rstd = rsqrtf(fmaf(ss, a.inv_hd, a.eps));
-          const float2 r2 = splat2(rstd);
-          if constexpr (BACK) {
-            // x^ = x rstd;  dx = rstd (h - x^ mean(x^ h))
-            const float2 k2 = splat2(-rstd * rstd * d * a.inv_hd);
-#pragma unroll
-            for (int m = 0; m < P; ++m) {
-              x[m] = mul2(x[m], r2);
-              if (live) dg[m] = fma2(o[m], x[m], dg[m]);
-              o[m] = fma2(x[m], k2, mul2(h[m], r2));
-            }
-          } else {
-#pragma unroll
-            for (int m = 0; m < P; ++m) o[m] = mul2(o[m], r2);
+            gam[2 * m] = ge;  // kept in the same split as the channels
+            gam[2 * m + 1] = go;
           }
         }
-        if (live) {
-          uint4 res;
+
+        // one head vector (dy with it in the norm's backward pass) to dst
+        auto turn = [&](uint4 vx, uint4 vg, bool live, unsigned char *dst) {
+          // v: the vector that is turned; o: the turned one
+          const uint4 v = BACK ? vg : vx;
+          float2 o[P];
           if constexpr (HALF) {
-            res = IO::pack(o);
+            uint4 vp;
+            vp.x = __shfl_sync(0xffffffffu, v.x, partner);
+            vp.y = __shfl_sync(0xffffffffu, v.y, partner);
+            vp.z = __shfl_sync(0xffffffffu, v.z, partner);
+            vp.w = __shfl_sync(0xffffffffu, v.w, partner);
+            float2 own[P], oth[P];
+            IO::unpack(v, own);
+            IO::unpack(vp, oth);
+#pragma unroll
+            for (int m = 0; m < P; ++m) o[m] = fma2(own[m], A[m], mul2(oth[m], B[m]));
           } else {
             float2 ev[P / 2], od[P / 2];
+            IO::unpack_eo(v, ev, od);
 #pragma unroll
             for (int m = 0; m < P / 2; ++m) {
-              ev[m] = o[2 * m];
-              od[m] = o[2 * m + 1];
+              if constexpr (BACK) {
+                const float2 neg = mul2(B[m], splat2(-1.f));
+                o[2 * m] = fma2(ev[m], A[m], mul2(od[m], B[m]));
+                o[2 * m + 1] = fma2(od[m], A[m], mul2(ev[m], neg));
+              } else {
+                o[2 * m] = fma2(ev[m], A[m], mul2(od[m], B[m]));
+                o[2 * m + 1] = fma2(od[m], A[m + P / 2], mul2(ev[m], B[m + P / 2]));
+              }
             }
-            res = IO::pack_eo(ev, od);
           }
-          st_stream16(dst, res);
-        }
-      };
-      unsigned char *out = static_cast<unsigned char *>(a.out[t].data) +
-                           (b * a.out[t].sb + r * a.out[t].sr + slot * a.out[t].sh) + gl * 16;
-      const int64_t ostep = a.out[t].sh * step;
-      int head = slot;
-      if constexpr (DGAMMA) {
-#pragma unroll 1
-        for (int i = 0; i < passes; ++i, head += step, out += ostep) {
-          produce();
-          cp_async_wait<D - 1>();
-          const uint4 *entry = ring + cons * (2 * kRopeThreads);
-          cons = cons + 1 == D ? 0 : cons + 1;
-          const bool live = active && head < a.heads[t];
-          uint4 vx = make_uint4(0, 0, 0, 0), vg = make_uint4(0, 0, 0, 0);
+          if constexpr (NORM) {
+            float2 x[P];
+            if constexpr (HALF) {
+              IO::unpack(vx, x);
+            } else {
+              float2 ev[P / 2], od[P / 2];
+              IO::unpack_eo(vx, ev, od);
+#pragma unroll
+              for (int m = 0; m < P / 2; ++m) {
+                x[2 * m] = ev[m];
+                x[2 * m + 1] = od[m];
+              }
+            }
+            float2 sq = splat2(0.f), dot = splat2(0.f), h[P];
+#pragma unroll
+            for (int m = 0; m < P; ++m) {
+              sq = fma2(x[m], x[m], sq);
+              if constexpr (BACK) {
+                h[m] = mul2(o[m], gam[m]);
+                dot = fma2(h[m], x[m], dot);
+              }
+            }
+            float ss = sq.x + sq.y, d = dot.x + dot.y;
+#pragma unroll
+            for (int w = G / 2; w > 0; w >>= 1) {
+              ss += __shfl_xor_sync(0xffffffffu, ss, w);
+              if constexpr (BACK) d += __shfl_xor_sync(0xffffffffu, d, w);
+            }
+            const float rstd = rsqrtf(fmaf(ss, a.inv_hd, a.eps));
+            const float2 r2 = splat2(rstd);
+            if constexpr (BACK) {
+              // x^ = x rstd;  dx = rstd (h - x^ mean(x^ h))
+              const float2 k2 = splat2(-rstd * rstd * d * a.inv_hd);
+#pragma unroll
+              for (int m = 0; m < P; ++m) {
+                x[m] = mul2(x[m], r2);
+                if (live) dg[m] = fma2(o[m], x[m], dg[m]);
+                o[m] = fma2(x[m], k2, mul2(h[m], r2));
+              }
+            } else {
+#pragma unroll
+              for (int m = 0; m < P; ++m) o[m] = mul2(o[m], r2);
+            }
+          }
           if (live) {
-            vx = entry[0];
-            vg = entry[kRopeThreads];
+            uint4 res;
+            if constexpr (HALF) {
+              res = IO::pack(o);
+            } else {
+              float2 ev[P / 2], od[P / 2];
+#pragma unroll
+              for (int m = 0; m < P / 2; ++m) {
+                ev[m] = o[2 * m];
+                od[m] = o[2 * m + 1];
+              }
+              res = IO::pack_eo(ev, od);
+            }
+            st_stream16(dst, res);
           }
-          turn(vx, vg, live, out);
-        }
-      } else {
-        const HeadsArg &in = BACK ? a.g[t] : a.x[t];
-        const unsigned char *src = static_cast<const unsigned char *>(in.data) +
-                                   (b * in.sb + r * in.sr + slot * in.sh) + gl * 16;
-        const int64_t istep = in.sh * step;
-        for (int i = 0; i < passes; i += D, head += D * step) {
-          uint4 v[D];
+        };
+        unsigned char *out = static_cast<unsigned char *>(a.out[t].data) +
+                             (b * a.out[t].sb + r * a.out[t].sr + slot * a.out[t].sh) + gl * 16;
+        const int64_t ostep = a.out[t].sh * step;
+        int head = slot;
+        if constexpr (DGAMMA) {
+#pragma unroll 1
+          for (int i = 0; i < passes; i += RV, head += RV * step, out += RV * ostep) {
+            produce();
+            cp_async_wait<D - 1>();
+            const uint4 *entry = ring + cons * (2 * RV * kRopeThreads);
+            cons = cons + 1 == D ? 0 : cons + 1;
 #pragma unroll
-          for (int u = 0; u < D; ++u) {
-            v[u] = make_uint4(0, 0, 0, 0);
-            if (active && head + u * step < a.heads[t]) v[u] = ld_head16(src + u * istep);
+            for (int u = 0; u < RV; ++u) {
+              if (i + u < passes) {  // the same for the whole warp
+                const bool live = active && head + u * step < a.heads[t];
+                uint4 vx = make_uint4(0, 0, 0, 0), vg = make_uint4(0, 0, 0, 0);
+                if (live) {
+                  vx = entry[2 * u * kRopeThreads];
+                  vg = entry[(2 * u + 1) * kRopeThreads];
+                }
+                turn(vx, vg, live, out + u * ostep);
+              }
+            }
           }
-          src += D * istep;
+        } else {
+          const HeadsArg &in = BACK ? a.g[t] : a.x[t];
+          const unsigned char *src = static_cast<const unsigned char *>(in.data) +
+                                     (b * in.sb + r * in.sr + slot * in.sh) + gl * 16;
+          const int64_t istep = in.sh * step;
+          for (int i = 0; i < passes; i += D, head += D * step) {
+            uint4 v[D];
 #pragma unroll
-          for (int u = 0; u < D; ++u)
-            if (i + u < passes)  // the same for the whole warp
-              turn(v[u], v[u], active && head + u * step < a.heads[t], out + u * ostep);
-          out += D * ostep;
+            for (int u = 0; u < D; ++u) {
+              v[u] = make_uint4(0, 0, 0, 0);
+              if (active && head + u * step < a.heads[t]) v[u] = ld_head16(src + u * istep);
+            }
+            src += D * istep;
+#pragma unroll
+            for (int u = 0; u < D; ++u)
+              if (i + u < passes)  // the same for the whole warp
+                turn(v[u], v[u], active && head + u * step < a.heads[t], out + u * ostep);
+            out += D * ostep;
+          }
         }
-      }
-      if constexpr (DGAMMA) {
+        if constexpr (DGAMMA) {
 #pragma unroll
-        for (int m = 0; m < P; ++m) {
-          float2 *sum = sums + (t * P + m) * kRopeThreads + tid;
-          *sum = add2(*sum, dg[m]);
+          for (int m = 0; m < P; ++m) {
+            float2 *sum = sums + (t * P + m) * kRopeThreads + tid;
+            *sum = add2(*sum, dg[m]);
+          }
         }
       }
     }
+    if constexpr (DGAMMA) cp_async_wait<0>();
   }
+
   if constexpr (DGAMMA) {
-    cp_async_wait<0>();
     if (a.partial) {
       // channel c of q and k: the groups' sums, added in order by one thread
       __syncthreads();
@@ -456,22 +476,21 @@ cudaError_t launch_t(RopeArgs &a, cudaStream_t stream, int *ctas) {
   auto *kern = &rope_axes_kernel<T, G, HALF, MODE, D>;
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidConfiguration;
-  // Warps per row: one while that fills the SMs, more while rows are few and
-  // heads are left to share.
-  const int heads = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
-  int wr = 0;
-  while ((1 << wr) < WARPS && (GW << wr) < heads && (a.rows << wr) < 16LL * sms) ++wr;
   constexpr int PITCH = G * Io<T>::E / 2;
-  const size_t smem = (DGAMMA ? static_cast<size_t>(kRopeThreads) * (D * 32 + Io<T>::E * 8) : 0) +
+  const size_t smem = (DGAMMA ? static_cast<size_t>(kRopeThreads) * (D * kRopeEntry * 32 + Io<T>::E * 8) : 0) +
                       static_cast<size_t>(WARPS) * 2 * PITCH * 4;
   const int per_sm = resident_blocks(reinterpret_cast<const void *>(kern), kRopeThreads, smem);
   if (per_sm <= 0) return cudaErrorInvalidConfiguration;
   int64_t grid = static_cast<int64_t>(per_sm) * sms;
-  const int64_t most = ((a.rows << wr) + WARPS - 1) / WARPS;
-  if (grid > most) grid = most;
   if (grid > kMaxRopeCtas) grid = kMaxRopeCtas;
+  const int64_t warps = grid * WARPS, whole = a.rows / warps * warps, tail = a.rows - whole;
+  const int heads = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
+  int wr = 0;
+  while ((1 << wr) < WARPS && (GW << wr) < heads && (tail << (wr + 1)) <= warps) ++wr;
+  if (whole == 0) grid = ((tail << wr) + WARPS - 1) / WARPS;
   *ctas = static_cast<int>(grid);
-  kern<<<static_cast<unsigned>(grid), kRopeThreads, smem, stream>>>(a, wr);
+  kern<<<static_cast<unsigned>(grid), kRopeThreads, smem, stream>>>(a, static_cast<int>(whole),
+                                                                   wr);
   return cudaGetLastError();
 }
 

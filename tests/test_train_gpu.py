@@ -48,6 +48,7 @@ ROWS = [
     (1, 4099, 4000, 128, BF),     # many more rows than CTAs
     (7, 613, 600, 1000, F32),
     (1, 1201, 1100, 5120, BF),
+    (40, 9, 5, 264, BF),          # more (sample, modality) keys than a CTA of the join takes
 ]
 ids = lambda c: "x".join(str(v).replace("torch.", "") for v in c)  # noqa: E731
 
@@ -312,6 +313,8 @@ ROPE = [
     (1, 700, 2, 1, 8, (1, 1), F32, False, False, False, torch.int32),
     (2, 65, 3, 2, 40, (16, 4), F32, True, False, False, torch.float32),
     (1, 400, 40, 40, 128, (16, 24, 24), BF, False, False, False, torch.int32),
+    (2, 2401, 3, 2, 64, (8, 12, 12), BF, True, False, False, torch.int32),   # a round and a tail
+    (1, 9001, 1, 3, 32, (10, 6), F32, False, True, False, torch.int64),
 ]
 
 
@@ -458,18 +461,61 @@ def test_calls_on_a_side_stream():
     del junk
 
 
+def test_two_threads_on_two_streams():
+    import threading
+    t, _ = _norm_case((1, 3000, 2500, 1024, BF), False)
+    br = act(1, 3000, 1024, BF, 8)
+    gate = vec((1, 2, 1024), 0, 0.3, BF, 9)
+    rng = _rng()
+
+    def work():
+        n = api.layer_norm_backward(t["dy"], t["x"], t["mean"], t["rstd"], t["gamma"], t["beta"],
+                                    t["scale"], n_video=2500)
+        return (*n, *api.dropout_residual_backward(n.dx, br, gate, 2500, 0.3, rng))
+
+    want = work()
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def run(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                got[i] = [work() for _ in range(20)]
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors
+    for runs in got.values():
+        for res in runs:
+            for a, b in zip(want, res):
+                assert torch.equal(a, b)
+
+
 def test_captured_graphs_draw_new_masks_and_share_nothing():
     B, L, D, nv = 1, 130, 512, 100
     h, br, do = act(B, L, D, BF, 1), act(B, L, D, BF, 2), act(B, L, D, BF, 3)
     gate, sc = vec((B, 2, D), 0, 0.3, BF, 4), vec((B, 2, D), 0, 0.3, BF, 5)
     rng = _rng()
+    plan, pos = api.RopeAxes(64, (10, 22)), torch.arange(2 * L, device=DEV).view(2, L)
+    gq = vec((64,), 1, 0.1, BF, 6)
 
     def step(site):
         out = api.dropout_residual(h, br, gate, nv, 0.3, rng, site=site)
         y, mean, rstd = api.layer_norm(out, scale=sc, shift=sc, n_video=nv)
-        g = api.layer_norm_backward(do, out, mean, rstd, scale=sc, n_video=nv, dres=do)
-        return (out, y, *api.dropout_residual_backward(g.dx, br, gate, nv, 0.3, rng, site=site),
-                g.dscale, g.dshift)
+        heads = y.view(B, L, 8, 64)
+        q, _ = api.rope_axes(heads, None, pos, plan, gq, qk_norm=True)
+        r = api.rope_axes_backward(q, None, pos, plan, heads, None, gq, qk_norm=True)
+        g = api.layer_norm_backward(r.dq.view(B, L, D), out, mean, rstd, scale=sc, n_video=nv,
+                                    dres=do)
+        return (out, y, q, *api.dropout_residual_backward(g.dx, br, gate, nv, 0.3, rng, site=site),
+                g.dscale, g.dshift, r.dq, r.dgamma_q)
 
     step(0)
     torch.cuda.synchronize()

@@ -523,10 +523,11 @@ def _rng_arg(rng: Optional[torch.Tensor], p: float, like: torch.Tensor):
 def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], site: int = 0,
             out: Optional[torch.Tensor] = None,
             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
-    """x / (1 - p) where the generator keeps the element, else 0; x: any
-    contiguous tensor.  The mask is a function of (seed, offset + site, the
-    element's index, p), with rng = (seed, offset) two int64 on x's device: the
-    gradient is dropout(dout, p, rng, site)."""
+    """x / (1 - p) where the generator keeps the element, else 0; x: a contiguous
+    tensor whose last dimension is one that layer_norm takes.  The mask is a
+    function of (seed, offset + site, the element's index, p), with rng = (seed,
+    offset) two int64 on x's device: the gradient is dropout(dout, p, rng,
+    site)."""
     if x.dim() < 1 or not x.is_contiguous():
         raise ValueError("x must be a contiguous tensor")
     po = _arg(out, x.shape, "out", x)

@@ -156,13 +156,14 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
       load_stats(it + 1, st_next);
       cp_async_wait<S - 1>();
 
-      // the row's two sums: layer norm (g, g * x^), RMS (x^2, g * x)
+      // the row's two sums: layer norm (g, g * (x - mean)), RMS (x^2, g * x); x -
+      // mean is formed first, which loses nothing when they are close
       float2 sum[R];
 #pragma unroll
       for (int q = 0; q < R; ++q) {
         float2 u = splat2(0.f), v = splat2(0.f);
         if (it * step + ty * R + q < count) {
-          const float2 r2 = splat2(st[q].y), off = splat2(-st[q].x * st[q].y);
+          const float2 neg = splat2(-st[q].x);
 #pragma unroll
           for (int k = 0; k < VPT; ++k) {
             if (ok(k)) {
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
                   v = fma2(g, x[m], v);
                 } else {
                   u = add2(g, u);
-                  v = fma2(g, fma2(x[m], r2, off), v);
+                  v = fma2(g, add2(x[m], neg), v);
                 }
               }
             }
@@ -213,11 +214,11 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
       for (int q = 0; q < R; ++q) {
         const int j = it * step + ty * R + q;
         if (j < count) {
-          // dx = rstd * g + a1 * x^ + a0
+          // dx = W * (rstd * dy) + a1 * (x - mean) + a0
           const float rstd = RMS ? rsqrtf(fmaf(sum[q].x, inv_D, a.eps)) : st[q].y;
-          const float m2 = (RMS ? rstd * sum[q].y : sum[q].y) * inv_D;
-          const float2 a1 = splat2(-rstd * m2), a0 = splat2(-rstd * sum[q].x * inv_D);
-          const float2 r2 = splat2(rstd), off = splat2(-st[q].x * rstd);
+          const float m2 = rstd * sum[q].y * inv_D;  // mean(g * x^)
+          const float2 a1 = splat2(-rstd * m2 * rstd), a0 = splat2(-rstd * sum[q].x * inv_D);
+          const float2 r2 = splat2(rstd), neg = splat2(-st[q].x);
           uint4 *out = reinterpret_cast<uint4 *>(dxc + (row + j) * row_bytes) + tx;
 #pragma unroll
           for (int k = 0; k < VPT; ++k) {
@@ -228,17 +229,17 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
               if constexpr (DRES) IO::unpack(*slot(cons, q, 2, k), o);
 #pragma unroll
               for (int m = 0; m < P; ++m) {
-                const float2 xh = RMS ? mul2(x[m], r2) : fma2(x[m], r2, off);
-                s1[k][m] = fma2(xh, d[m], s1[k][m]);
+                if constexpr (!RMS) x[m] = add2(x[m], neg);
+                const float2 rd = mul2(d[m], r2);
+                s1[k][m] = fma2(x[m], rd, s1[k][m]);
                 s0[k][m] = add2(s0[k][m], d[m]);
-                const float2 g = mul2(d[m], W[k][m]);
                 if constexpr (DRES) {
-                  o[m] = fma2(xh, a1, o[m]);
+                  o[m] = fma2(x[m], a1, o[m]);
                   if constexpr (!RMS) o[m] = add2(o[m], a0);
                 } else {
-                  o[m] = RMS ? mul2(xh, a1) : fma2(xh, a1, a0);
+                  o[m] = RMS ? mul2(x[m], a1) : fma2(x[m], a1, a0);
                 }
-                o[m] = fma2(g, r2, o[m]);
+                o[m] = fma2(rd, W[k][m], o[m]);
               }
               st_stream16(out + k * NT, IO::pack(o));
             }
@@ -339,11 +340,7 @@ cudaError_t launch_t(NormBwdArgs &a, cudaStream_t stream) {
 // threads), then as few as 512 threads can hold.
 template <typename T, bool RMS, bool DRES>
 cudaError_t dispatch(NormBwdArgs &a, cudaStream_t stream) {
-#ifndef NB_V1
-#define NB_V1 0
-#endif
-  const int nt1 = (a.nvec + 31) / 32 * 32, nt2 = ((a.nvec + 1) / 2 + 31) / 32 * 32;
-  if (a.nvec <= 32 || (NB_V1 == 1 && a.nvec <= 320) || (NB_V1 == 2 && a.nvec <= 320 && nt1 < 2 * nt2)) return launch_t<T, 1, RMS, DRES>(a, stream);
+  if (a.nvec <= 32) return launch_t<T, 1, RMS, DRES>(a, stream);
   if (a.nvec <= 640) return launch_t<T, 2, RMS, DRES>(a, stream);
   if (a.nvec <= 1536) return launch_t<T, 3, RMS, DRES>(a, stream);
   return launch_t<T, 4, RMS, DRES>(a, stream);

@@ -3,7 +3,8 @@ for profilers (ncu) that should capture a small, self-contained case.
 
     python -m video_diffusion_transformer_rms_b200.profile_case \
         [--workload clip5s] [--frames 4] [--launches 1]
-        [--kernel norm|rms|gate|qk|qk_tab|gemm|qk_bhsd|qk_half|qk_int8|qk_all|next] [--table]
+        [--kernel norm|rms|gate|qk|qk_tab|gemm|qk_bhsd|qk_half|qk_int8|qk_all|next|
+                  train|ln|ln_bwd|rms_bwd|drop|drop_bwd|rope|rope_bwd] [--table]
 
 The slice keeps the clip's H x W latent grid, D and head layout, takes the
 first `--frames` latent frames (T) and scales the audio rows by the same
@@ -18,7 +19,9 @@ quantised v, one launch each), and `--kernel next` the fused residual +
 RMS-AdaLN and the change detector (read-only, then with the cache refresh).
 `--kernel norm` runs the step's three kernels; `rms`, `gate`, `qk` (per-row
 cos/sin) and `qk_tab` (rotary table) one of them alone, for captures that
-must hold a single kernel.  `--table` makes the qk_* variants read a rotary
+must hold a single kernel.  `--kernel train` runs every training operator,
+`ln` .. `rope_bwd` one of them alone (layer norm with AdaLN modulation, dropout
+with p = 0.1, rotation at position ids behind QKNorm).  `--table` makes the qk_* variants read a rotary
 table too.  The slice prints its row count (the scale factor to the full
 workload's traffic).
 """
@@ -31,6 +34,9 @@ from . import _abi, api
 from .workloads import WORKLOADS, make_inputs
 
 
+TRAIN = ("ln", "ln_bwd", "rms_bwd", "drop", "drop_bwd", "rope", "rope_bwd")
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--workload", default="clip5s", choices=sorted(WORKLOADS))
@@ -38,7 +44,7 @@ def main():
     ap.add_argument("--launches", type=int, default=1)
     ap.add_argument("--kernel", default="norm",
                     choices=["norm", "rms", "gate", "qk", "qk_tab", "gemm", "qk_bhsd", "qk_half",
-                             "qk_int8", "qk_all", "next"])
+                             "qk_int8", "qk_all", "next", "train", *TRAIN])
     ap.add_argument("--table", action="store_true",
                     help="QKNorm+RoPE variants read a precomputed rotary table")
     args = ap.parse_args()
@@ -48,6 +54,8 @@ def main():
     w = dataclasses.replace(full, name=f"{full.name}_slice{T}", T=T, n_audio=n_audio)
     if args.kernel == "gemm":
         return gemm_case(w, args.launches)
+    if args.kernel == "train" or args.kernel in TRAIN:
+        return train_case(w, args.kernel, args.launches)
     t = make_inputs(w, "cuda")
     D = w.D
     x = t["x"].view(w.B, w.L, D)
@@ -109,6 +117,42 @@ def main():
         api.gate_residual(h, br, t["gate"], w.n_video, out=out)
     torch.cuda.synchronize()
     print(f"{w.name}: {w.rows} rows, D={D}, {args.launches} launch(es) of each kernel")
+
+
+def train_case(w, which, launches):
+    """The training operators on the slice: each of TRAIN, or one of them."""
+    names = TRAIN if which == "train" else (which,)
+    t = make_inputs(w, "cuda")
+    shape = (w.B, w.L, w.D)
+    x, h, br = (t[n].view(shape) for n in ("x", "h", "branch"))
+    rng = torch.tensor([1, 2], device="cuda")
+    mean = x.float().mean(-1)
+    rstd = (x.float().var(-1, correction=0) + w.eps).rsqrt()
+    heads = t["qkv"].view(w.B, w.L, 3, w.n_heads, w.head_dim)
+    q, k = heads[:, :, 0], heads[:, :, 1]
+    r = torch.arange(w.L, device="cuda", dtype=torch.int32)
+    grid, hw = r < w.n_video, w.H * w.W
+    pos = torch.stack([torch.where(grid, r // hw, r - w.n_video),
+                       torch.where(grid, r // w.W % w.H, 0), torch.where(grid, r % w.W, 0)])
+    plan = api.RopeAxes(w.head_dim, w.sections, theta=w.theta)
+    gq, gk = t["gamma_q"], t["gamma_k"]
+    dq = torch.randn_like(q, memory_format=torch.contiguous_format)
+    calls = {
+        "ln": lambda: api.layer_norm(x, scale=t["scale"], shift=t["shift"], n_video=w.n_video),
+        "ln_bwd": lambda: api.layer_norm_backward(h, x, mean, rstd, scale=t["scale"],
+                                                  n_video=w.n_video),
+        "rms_bwd": lambda: api.rms_adaln_backward(h, x, t["scale"], w.n_video, eps=w.eps),
+        "drop": lambda: api.dropout_residual(h, br, t["gate"], w.n_video, 0.1, rng),
+        "drop_bwd": lambda: api.dropout_residual_backward(h, br, t["gate"], w.n_video, 0.1, rng),
+        "rope": lambda: api.rope_axes(q, k, pos, plan, gq, gk, qk_norm=True, eps=w.eps),
+        "rope_bwd": lambda: api.rope_axes_backward(dq, dq, pos, plan, q, k, gq, gk, qk_norm=True,
+                                                   eps=w.eps),
+    }
+    for _ in range(launches):
+        for n in names:
+            calls[n]()
+    torch.cuda.synchronize()
+    print(f"{w.name}: {w.rows} rows, D={w.D}, {launches} launch(es) of {', '.join(names)}")
 
 
 def gemm_case(w, launches):

@@ -97,29 +97,6 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
     const int step = RG * R;  // rows of one iteration: group ty takes R of them
     const int iters = (count + step - 1) / step;
 
-    float2 W[VPT][P], s1[VPT][P], s0[VPT][P];
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-#pragma unroll
-      for (int m = 0; m < P; ++m) {
-        W[k][m] = splat2(1.f);
-        s1[k][m] = splat2(0.f);
-        s0[k][m] = splat2(0.f);
-      }
-      if (ok(k)) {
-        if (a.gamma)
-          IO::unpack(ld_shared_vec(static_cast<const uint4 *>(a.gamma) + k * NT + tx), W[k]);
-        if (a.scale) {
-          float2 sc[P];
-          IO::unpack(ld_shared_vec(static_cast<const uint4 *>(a.scale) +
-                                   static_cast<int64_t>(key) * a.nvec + k * NT + tx),
-                     sc);
-#pragma unroll
-          for (int m = 0; m < P; ++m) W[k][m] = mul2(W[k][m], add2(sc[m], splat2(1.f)));
-        }
-      }
-    }
-
     auto issue = [&](int it, int s) {
 #pragma unroll
       for (int q = 0; q < R; ++q) {
@@ -149,6 +126,29 @@ __global__ void __launch_bounds__(kNormThreads<VPT>, kNormCtas<VPT>)
     for (int s = 0; s < S - 1; ++s) issue(s, s);
     float2 st[R], st_next[R];
     load_stats(0, st);
+
+    float2 W[VPT][P], s1[VPT][P], s0[VPT][P];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+#pragma unroll
+      for (int m = 0; m < P; ++m) {
+        W[k][m] = splat2(1.f);
+        s1[k][m] = splat2(0.f);
+        s0[k][m] = splat2(0.f);
+      }
+      if (ok(k)) {
+        if (a.gamma)
+          IO::unpack(ld_shared_vec(static_cast<const uint4 *>(a.gamma) + k * NT + tx), W[k]);
+        if (a.scale) {
+          float2 sc[P];
+          IO::unpack(ld_shared_vec(static_cast<const uint4 *>(a.scale) +
+                                   static_cast<int64_t>(key) * a.nvec + k * NT + tx),
+                     sc);
+#pragma unroll
+          for (int m = 0; m < P; ++m) W[k][m] = mul2(W[k][m], add2(sc[m], splat2(1.f)));
+        }
+      }
+    }
 
     int cons = 0;
     for (int it = 0; it < iters; ++it) {

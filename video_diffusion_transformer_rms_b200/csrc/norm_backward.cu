@@ -328,8 +328,7 @@ cudaError_t launch_full(NormBwdArgs &a, cudaStream_t stream) {
 }
 
 // RMS rows that fill every thread's vectors take the unguarded instantiation
-// (0.716 -> 0.672 ms at the 5 s clip, and -> 0.643 on another box); the layer norm
-// was 2% slower with it.
+// (0.716 -> 0.672 ms at the 5 s clip); the layer norm was 2% slower with it.
 template <typename T, int VPT, bool RMS, bool DRES>
 cudaError_t launch_t(NormBwdArgs &a, cudaStream_t stream) {
   return RMS && a.nvec % (32 * VPT) == 0 ? launch_full<T, VPT, RMS, DRES, RMS>(a, stream)

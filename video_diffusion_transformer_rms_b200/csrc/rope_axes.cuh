@@ -14,9 +14,9 @@
 // few rotary pairs each, once for all q and k heads: the product in fp64, reduced
 // to [-pi, pi] by a two-part 2 pi, then sin and cos of the fp32 rest, corrected
 // to first order by what that rounding dropped.  They meet in the warp's own
-// shared memory, so nothing waits for another warp.  Then G consecutive lanes own one head vector at a
-// time (16 bytes per lane; G is the next power of two, lanes past head_dim
-// idle).  A lane sees the same channels in every head: its cos and sin, with
+// shared memory, so nothing waits for another warp.  Then G consecutive lanes
+// own one head vector at a time (16 bytes per lane; G is the next power of two,
+// lanes past head_dim idle).  A lane sees the same channels in every head: its cos and sin, with
 // gamma folded in, stay in registers for the row.  Several vectors per lane are
 // in flight: as a batch of loads into registers, or, in the norm's backward
 // pass, which needs the registers for its sums and two vectors per head, through
@@ -52,7 +52,8 @@ __device__ __forceinline__ uint4 ld_head16(const void *p) {
   return v;
 }
 
-// cos and sin of pos * freq.
+// cos and sin of pos * freq.  (Reduced to a part of a turn and sincospif: 3 to
+// 11% slower in calls of few rows, which wait for the angles.)
 __device__ __forceinline__ float2 cos_sin(double pos, double freq) {
   const double ang = pos * freq;
   const double turns = rint(ang * 0.15915494309189533577);      // 1 / (2 pi)
@@ -73,11 +74,11 @@ template <int MODE>
 constexpr int kRopeMinCtas = MODE == kNormRotateBack ? 2 : 3;
 // Depth of the loads in flight: vectors per lane, or in the norm's backward pass
 // ring entries of kRopeEntry heads each, which spread the ring's bookkeeping.
-// 5 s clip, half-split / interleaved: 3 entries of 3 heads 1.233 / 1.247 ms, 4 of
-// 2 1.307 / 1.186, 2 of 4 1.231 / 1.287, 6 of 1 1.345 / 1.261.
+// Under the power cap (5 s clip, half-split / interleaved): 2 entries of 4 heads
+// 1.365 / 1.314 ms, of 5 1.367 / 1.312, 3 of 3 1.393 / 1.332, 4 of 2 1.395 / -.
 template <int MODE>
-constexpr int kRopeDepth = MODE == kNormRotateBack ? 3 : 4;
-constexpr int kRopeEntry = 3;
+constexpr int kRopeDepth = MODE == kNormRotateBack ? 2 : 4;
+constexpr int kRopeEntry = 4;
 
 // MODE as RopeMode.  HALF: pair i = channels (i, i + rot_dim / 2), else
 // (2i, 2i + 1).  The rows from whole_rows on are shared by 2^tail_log2 warps.
@@ -477,7 +478,8 @@ cudaError_t launch_t(RopeArgs &a, cudaStream_t stream, int *ctas) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidConfiguration;
   constexpr int PITCH = G * Io<T>::E / 2;
-  const size_t smem = (DGAMMA ? static_cast<size_t>(kRopeThreads) * (D * kRopeEntry * 32 + Io<T>::E * 8) : 0) +
+  const size_t ring = static_cast<size_t>(kRopeThreads) * (D * kRopeEntry * 32 + Io<T>::E * 8);
+  const size_t smem = (DGAMMA ? ring : 0) +
                       static_cast<size_t>(WARPS) * 2 * PITCH * 4;
   const int per_sm = resident_blocks(reinterpret_cast<const void *>(kern), kRopeThreads, smem);
   if (per_sm <= 0) return cudaErrorInvalidConfiguration;

@@ -209,10 +209,10 @@ __global__ void __launch_bounds__(NT, kLnThreadsPerSm<VPT> / NT < 16 ? kLnThread
 
 // Chunk of consecutive rows per CTA turn, as RMS-AdaLN's.
 constexpr int kLnChunk = 8;
-// Rows of the ring.  Under the power cap, 5 s clip: three single rows 0.438 ms,
-// two pairs of rows 0.470 (the pairs share a barrier, but leave the ring one
-// step ahead).
-constexpr int kLnStages = 3;
+// Rows of the ring.  5 s clip, in short runs / in long ones under the power cap:
+// 3 rows 0.458 / 0.444 ms, 4 rows 0.430 / 0.445, 5 rows 0.455 / 0.468; two pairs
+// of rows, which share a barrier but leave the ring one step ahead, 0.427 / 0.470.
+constexpr int kLnStages = 4;
 
 template <typename T, int NT, int VPT, bool FULL>
 cudaError_t launch_t(const LnArgs &a, cudaStream_t stream) {
@@ -227,8 +227,8 @@ cudaError_t launch_t(const LnArgs &a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// A split that covers the row exactly takes the unguarded instantiation: 0.438
-// against 0.449 ms at the 5 s clip, 36.2 us either way at 8,264 rows.
+// A split that covers the row exactly takes the unguarded instantiation: 2.5%
+// faster at the 5 s clip (three rows in the ring), the same at 8,264 rows.
 template <typename T>
 cudaError_t dispatch(const LnArgs &a, int threads, int vpt, cudaStream_t stream) {
 #define SOL_CASE(NT, V)                                                \

@@ -653,8 +653,8 @@ typedef struct sol_positions {
 
 /* Head vectors: channel c of head h of row r of sample b is element
  * b*stride_b + r*stride_row + h*stride_head + c.  Strides are >= 0 and, like
- * data, multiples of 16 bytes; those of an output must address distinct
- * elements (not checked). */
+ * data, multiples of 16 bytes.  An output's address distinct elements: in
+ * order of their strides, each of its axes steps over all below it. */
 typedef struct sol_heads {
     void *data;         /* device */
     int64_t n_heads;    /* 1 .. 1024 */

@@ -631,3 +631,44 @@ def test_clip_sized_gradients_on_sampled_rows():
             s[1] += torch.stack([d.sum(0), d.abs().sum(0)])
         ref.check(got.dscale[0, m], (s[0, 0], s[0, 1]), ref.depth_rows(428), "dscale")
         ref.check(got.dshift[0, m], (s[1, 0], s[1, 1]), ref.depth_rows(428), "dshift")
+
+
+def test_more_elements_than_32_bits_count():
+    # 2^20 + 3 rows of 57 heads of 72: 4.3e9 elements, 8.6 GB each tensor
+    L, H, hd = 2 ** 20 + 3, 57, 72
+    nv, D = L - 2, H * hd
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x, dy = (torch.empty((1, L, D), dtype=BF, device=DEV).normal_(generator=g) for _ in "xy")
+    sc, sh = vec((1, 2, D), 0, 0.5, BF, 3), vec((1, 2, D), 0, 0.5, BF, 4)
+    pick = torch.tensor([0, 1, L // 2, L - 130, nv - 1, nv, L - 1], device=DEV)
+    nvp = 5
+    px, pdy = x[:, pick], dy[:, pick]
+    y, mean, rstd = api.layer_norm(x, scale=sc, shift=sh, n_video=nv, eps=EPS)
+    ref.check(y[:, pick], ref.layer_norm(px, None, None, sc, sh, nvp, EPS)[0], ref.depth_row(D),
+              "y")
+    got = api.layer_norm_backward(dy, x, mean, rstd, scale=sc, n_video=nv, dx=y)
+    args = (sc, None, nvp, EPS)
+    want = ref.norm_backward(pdy, px, mean[:, pick], rstd[:, pick], None, None, *args, False)["dx"]
+    ref.check(got.dx[:, pick], want, ref.depth_row(D), "dx")
+    api.rms_adaln_backward(dy, x, sc, nv, eps=EPS, dx=y)
+    want = ref.norm_backward(pdy, px, None, None, None, None, *args, True)["dx"]
+    ref.check(y[:, pick], want, ref.depth_row(D), "dx of the RMS norm")
+
+    rng, p = _rng(), 0.25
+    keep = torch.stack([ref.keep_mask(D, *RNG, p, DEV, first=int(r) * D) for r in pick])[None]
+    d = torch.where(keep, px.double(), 0.0) / (1 - ref.p32(p)) * ref.spread(sc, nvp, 7)
+    api.dropout_residual(dy, x, sc, nv, p, rng, out=y)
+    ref.check(y[:, pick], (d + pdy.double(), d.abs() + pdy.double().abs()), 4, "out")
+    api.dropout_residual_backward(x, dy, sc, nv, p, rng, dbranch=y)
+    ref.check(y[:, pick], (d, d.abs()), 4, "dbranch")
+
+    pos = (torch.arange(L, device=DEV, dtype=torch.int32) % 4099)[None]
+    plan, pairs = api.RopeAxes(hd, (36,)), ref.pair_map((36,), 10000.0, False, False)
+    ppos, hx, hdy = pos[:, None, pick], x.view(1, L, H, hd), dy.view(1, L, H, hd)
+    api.rope_axes(hx, None, pos, plan, qk_norm=True, eps=EPS, q_out=y.view(1, L, H, hd))
+    want = ref.rope(hx[:, pick], ppos, pairs, False, True, None, EPS)
+    ref.check(y.view(1, L, H, hd)[:, pick], want, 32, "rotated")
+    api.rope_axes_backward(hdy, None, pos, plan, hx, qk_norm=True, eps=EPS,
+                           dq=y.view(1, L, H, hd))
+    want, _ = ref.rope_backward(hdy[:, pick], hx[:, pick], ppos, pairs, False, True, None, EPS)
+    ref.check(y.view(1, L, H, hd)[:, pick], want, 48, "dq")

@@ -301,6 +301,25 @@ def test_rope_refused(kw, status):
     assert _abi.last_error()
 
 
+# outputs whose own elements overlap, in place too; positions out of range
+@pytest.mark.parametrize("kw", [
+    dict(qo=H(A + 2 * G, sh=0)), dict(qo=H(A + 2 * G, sh=64)), dict(qo=H(A + 2 * G, sr=128)),
+    dict(qo=H(A + 2 * G, sr=0)), dict(qo=H(A + 2 * G, sb=256)), dict(ko=H(A + 3 * G, sb=0)),
+    dict(qo=H(A + 2 * G, sb=128, sr=128, sh=1024)), dict(q=H(A, sb=0), qo=H(A, sb=0)),
+    dict(pos=P(sa=2 ** 62)), dict(pos=P(sb=2 ** 62)), dict(pos=P(sb=2 ** 40), B=2 ** 29, L=1),
+])
+def test_rope_refuses_overlapping_outputs_and_far_positions(kw):
+    assert rope(**kw) == INV
+    assert _abi.last_error()
+
+
+def test_rope_empty_and_reordered_axes_are_not_refused():
+    # no rows: nothing to overlap; and axes in another order of strides are in order
+    assert rope(qo=H(A + 2 * G, sh=0), L=0) == 0
+    assert rope(qo=H(A + 2 * G, sb=1024, sr=128, sh=512), ko=H(A + 3 * G, n=3)) == INV
+    assert "heads" in _abi.last_error() and "overlap" not in _abi.last_error()
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(dqo=None), INV), (dict(dq=None), INV), (dict(q=None), INV), (dict(k=None), INV),
     (dict(dk=None), INV), (dict(norm=0), INV),

@@ -1,8 +1,10 @@
 // C ABI of the training operators (declared in include/sol.h): host-side
 // argument checks, then the launches on the caller's stream.  Nothing is
 // allocated on the device and nothing is synchronised.
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <utility>
 
 #include "sol.h"
 #include "sol_check.h"
@@ -258,6 +260,21 @@ bool same_heads(const sol_heads &a, const sol_heads &b) {
          a.stride_head == b.stride_head && a.n_heads == b.n_heads;
 }
 
+// True if no two elements of the array share an address: with the axes in order of
+// their strides, each steps over all that lies below it.
+bool heads_separate(const sol_heads &h, int64_t B, int64_t L, int head_dim) {
+  std::pair<int64_t, int64_t> ax[3] = {
+      {h.stride_b, B}, {h.stride_row, L}, {h.stride_head, h.n_heads}};
+  std::sort(ax, ax + 3);
+  __int128 extent = head_dim;
+  for (const auto &[stride, n] : ax) {
+    if (n < 2) continue;
+    if (stride < extent) return false;
+    extent += static_cast<__int128>(n - 1) * stride;
+  }
+  return true;
+}
+
 // True if the two share no byte: apart in memory, or column blocks of rows of
 // one pitch (q, k and v of a merged projection).
 bool heads_disjoint(const sol_heads &a, const sol_heads &b, int64_t B, int64_t L, int head_dim,
@@ -323,8 +340,7 @@ sol_status rope_args(const char *fn, const sol_rope_plan *plan, const sol_positi
   if (!out[1] && gamma_k)
     return fail(SOL_ERR_INVALID_ARG, "%s: gamma_k without k", fn);
   if (!pos || pos->type < SOL_POS_I32 || pos->type > SOL_POS_F32 || pos->reserved != 0 ||
-      pos->stride_axis < 0 || pos->stride_b < 0 || pos->stride_axis > (int64_t(1) << 40) ||
-      pos->stride_b > (int64_t(1) << 40))
+      pos->stride_axis < 0 || pos->stride_b < 0)
     return fail(SOL_ERR_INVALID_ARG, "%s: bad positions", fn);
   if (B * L == 0) {
     empty = true;
@@ -345,9 +361,14 @@ sol_status rope_args(const char *fn, const sol_rope_plan *plan, const sol_positi
       st = check_heads(fn, name, h, a.heads[t], B, L, hd, es);
       if (st != SOL_OK) return st;
     }
+    if (!heads_separate(*out[t], B, L, hd))
+      return fail(SOL_ERR_INVALID_ARG, "%s: the strides of an output make its heads overlap", fn);
   }
-  const int64_t pos_bytes =
-      ((plan->n_axes - 1) * pos->stride_axis + (B - 1) * pos->stride_b + L) * pes;
+  const __int128 n_pos = static_cast<__int128>(plan->n_axes - 1) * pos->stride_axis +
+                         static_cast<__int128>(B - 1) * pos->stride_b + L;
+  if (n_pos > (static_cast<__int128>(1) << 56))
+    return fail(SOL_ERR_INVALID_ARG, "%s: positions have a stride out of range", fn);
+  const int64_t pos_bytes = static_cast<int64_t>(n_pos) * pes;
   const Arr small[] = {{"positions", pos->data, pos_bytes},
                        {"gamma_q", gamma_q, static_cast<int64_t>(hd) * es},
                        {"gamma_k", gamma_k, static_cast<int64_t>(hd) * es}};

@@ -136,7 +136,7 @@ def train_case(w, which, launches):
                        torch.where(grid, r // w.W % w.H, 0), torch.where(grid, r % w.W, 0)])
     plan = api.RopeAxes(w.head_dim, w.sections, theta=w.theta)
     gq, gk = t["gamma_q"], t["gamma_k"]
-    dq = torch.randn_like(q, memory_format=torch.contiguous_format)
+    dq, dk = (torch.randn_like(q, memory_format=torch.contiguous_format) for _ in "qk")
     calls = {
         "ln": lambda: api.layer_norm(x, scale=t["scale"], shift=t["shift"], n_video=w.n_video),
         "ln_bwd": lambda: api.layer_norm_backward(h, x, mean, rstd, scale=t["scale"],
@@ -145,7 +145,7 @@ def train_case(w, which, launches):
         "drop": lambda: api.dropout_residual(h, br, t["gate"], w.n_video, 0.1, rng),
         "drop_bwd": lambda: api.dropout_residual_backward(h, br, t["gate"], w.n_video, 0.1, rng),
         "rope": lambda: api.rope_axes(q, k, pos, plan, gq, gk, qk_norm=True, eps=w.eps),
-        "rope_bwd": lambda: api.rope_axes_backward(dq, dq, pos, plan, q, k, gq, gk, qk_norm=True,
+        "rope_bwd": lambda: api.rope_axes_backward(dq, dk, pos, plan, q, k, gq, gk, qk_norm=True,
                                                    eps=w.eps),
     }
     for _ in range(launches):

@@ -24,9 +24,7 @@
 namespace sol {
 namespace {
 
-// A staged vector, read again at each use: holding a row's unpacked channels
-// across the reductions took 252 registers at 128 x 5 and left 8 warps on an
-// SM (0.469 ms at the 5 s clip).
+// A staged vector, read from shared memory at every use.
 __device__ __forceinline__ uint4 ld_staged(const uint4 *p) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -37,9 +35,16 @@ __device__ __forceinline__ uint4 ld_staged(const uint4 *p) {
 }
 
 // Threads per SM that the registers are to leave room for: 128 registers a
-// thread while its vectors fit them.
+// thread while its vectors fit them (102: 0.75 ms at the 5 s clip, spilled).
 template <int VPT>
 constexpr int kLnThreadsPerSm = VPT <= 5 ? 512 : 256;
+
+// A row of up to four vectors per thread stays in registers across the two
+// reductions; a wider one is read from shared memory again for each.  5 s clip in
+// short runs / in long ones under the power cap, 8,264 rows: 160 x 4 held 0.405 /
+// 0.426 ms, 32.5 us; 128 x 5 read again 0.422 / 0.421 ms, 34.6 us.  (Held, 128 x 5
+// takes 252 registers: 0.469 ms.)
+constexpr int kLnHeld = 4;
 
 // FULL: the split covers the row exactly, no access needs a guard.
 template <typename T, int NT, int VPT, int S, int K, bool FULL>
@@ -48,6 +53,7 @@ __global__ void __launch_bounds__(NT, kLnThreadsPerSm<VPT> / NT < 16 ? kLnThread
   using IO = Io<T>;
   constexpr int P = IO::E / 2;
   constexpr int NW = NT / 32;
+  constexpr bool HOLD = VPT <= kLnHeld;
   extern __shared__ __align__(16) unsigned char smem[];
   float4 *red = reinterpret_cast<float4 *>(smem);               // [2][NW]: sum, M2, mean, n
   uint4 *ring = reinterpret_cast<uint4 *>(smem + 2 * NW * 16);  // [S][VPT][NT]
@@ -135,12 +141,22 @@ __global__ void __launch_bounds__(NT, kLnThreadsPerSm<VPT> / NT < 16 ? kLnThread
     }
     cp_async_wait<S - 1>();
 
+    float2 held[HOLD ? VPT : 1][P];
+    auto channels = [&](int k, float2 (&x)[P]) {
+      if constexpr (HOLD) {
+#pragma unroll
+        for (int m = 0; m < P; ++m) x[m] = held[k][m];
+      } else {
+        IO::unpack(ld_staged(slot(cons, k)), x);
+      }
+    };
     float2 acc = splat2(0.f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       if (ok[k]) {
+        if constexpr (HOLD) IO::unpack(ld_staged(slot(cons, k)), held[k]);
         float2 x[P];
-        IO::unpack(ld_staged(slot(cons, k)), x);
+        channels(k, x);
 #pragma unroll
         for (int m = 0; m < P; ++m) acc = add2(x[m], acc);
       }
@@ -153,7 +169,7 @@ __global__ void __launch_bounds__(NT, kLnThreadsPerSm<VPT> / NT < 16 ? kLnThread
     for (int k = 0; k < VPT; ++k) {
       if (ok[k]) {
         float2 x[P];
-        IO::unpack(ld_staged(slot(cons, k)), x);
+        channels(k, x);
 #pragma unroll
         for (int m = 0; m < P; ++m) {
           const float2 d = add2(x[m], neg);
@@ -190,7 +206,7 @@ __global__ void __launch_bounds__(NT, kLnThreadsPerSm<VPT> / NT < 16 ? kLnThread
     for (int k = 0; k < VPT; ++k) {
       if (ok[k]) {
         float2 x[P], o[P];
-        IO::unpack(ld_staged(slot(cons, k)), x);
+        channels(k, x);
 #pragma unroll
         for (int m = 0; m < P; ++m)
           o[m] = fma2(add2(x[m], neg), mul2(fac[k][m], inv2), off[k][m]);
@@ -209,10 +225,11 @@ __global__ void __launch_bounds__(NT, kLnThreadsPerSm<VPT> / NT < 16 ? kLnThread
 
 // Chunk of consecutive rows per CTA turn, as RMS-AdaLN's.
 constexpr int kLnChunk = 8;
-// Rows of the ring.  5 s clip, in short runs / in long ones under the power cap:
-// 3 rows 0.458 / 0.444 ms, 4 rows 0.430 / 0.445, 5 rows 0.455 / 0.468; two pairs
-// of rows, which share a barrier but leave the ring one step ahead, 0.427 / 0.470.
-constexpr int kLnStages = 4;
+// Rows of the ring: one ahead.  More in flight is slower where the tensors are far
+// larger than L2 (160 x 4, short / long runs at the 5 s clip: 2 rows 0.405 /
+// 0.426 ms, 3 rows 0.459 / 0.422, 4 rows 0.472 / 0.462; 250,000 rows of 2,048
+// bf16: 0.330, 0.373 and 0.376), and none ahead waits (0.558).
+constexpr int kLnStages = 2;
 
 template <typename T, int NT, int VPT, bool FULL>
 cudaError_t launch_t(const LnArgs &a, cudaStream_t stream) {
@@ -227,15 +244,16 @@ cudaError_t launch_t(const LnArgs &a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// A split that covers the row exactly takes the unguarded instantiation: 2.5%
-// faster at the 5 s clip (three rows in the ring), the same at 8,264 rows.
+// Four vectors per thread up to 256 threads, then more.  A split that covers the
+// row exactly takes the unguarded instantiation: 2.5% faster at the 5 s clip (with
+// 128 x 5), the same at 8,264 rows.
 template <typename T>
 cudaError_t dispatch(const LnArgs &a, int threads, int vpt, cudaStream_t stream) {
 #define SOL_CASE(NT, V)                                                \
   if (threads == NT && vpt == V)                                       \
     return a.nvec == NT * V ? launch_t<T, NT, V, true>(a, stream)      \
                             : launch_t<T, NT, V, false>(a, stream);
-  SOL_SPLITS(SOL_CASE)
+  SOL_QK_OTF_SPLITS(SOL_CASE)
 #undef SOL_CASE
   return cudaErrorInvalidValue;
 }
@@ -244,7 +262,7 @@ cudaError_t dispatch(const LnArgs &a, int threads, int vpt, cudaStream_t stream)
 
 cudaError_t launch_layer_norm(const LnArgs &a, int dtype, cudaStream_t stream) {
   int threads = 0, vpt = 0;
-  if (!pick_split(a.nvec, &threads, &vpt)) return cudaErrorInvalidValue;
+  if (!pick_split_otf(a.nvec, &threads, &vpt)) return cudaErrorInvalidValue;
   return dtype == 0 ? dispatch<float>(a, threads, vpt, stream)
                     : dispatch<__nv_bfloat16>(a, threads, vpt, stream);
 }

@@ -306,10 +306,13 @@ template <typename T, int VPT, bool RMS, bool DRES, bool FULL>
 cudaError_t launch_full(NormBwdArgs &a, cudaStream_t stream) {
   // Rows per group and stages.  One row where a third input is staged (two
   // would leave shared memory for one CTA per SM) and in RMS (0.654 against
-  // 0.678 ms for two at the 5 s clip; the layer norm 0.743 against 0.649 ms);
-  // wider rows take what fits.
+  // 0.678 ms for two at the 5 s clip; the layer norm 0.743 against 0.649 ms).
+  // Three stages of one row, two where the rows come in pairs or with a third
+  // input (RMS at the 5 s clip: 3 stages 0.625 ms, 4 0.629, 2 0.624 and slower at
+  // 8,264 rows; layer norm of 60,000 rows of 4,096 fp32: 3 stages 0.483 ms, 2
+  // 0.518).
   constexpr int R = VPT > 2 || DRES || RMS ? 1 : 2;
-  constexpr int S = VPT <= 2 && RMS && !DRES ? 4 : 2;
+  constexpr int S = R == 2 || DRES ? 2 : 3;
   const int NT = ((a.nvec + VPT - 1) / VPT + 31) / 32 * 32;
   const int RG = NT >= 256 ? 1 : 256 / NT;
   auto *kern = &norm_backward_kernel<T, VPT, RMS, DRES, FULL, R, S>;

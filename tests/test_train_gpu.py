@@ -71,6 +71,23 @@ def test_layer_norm(case, affine, mod):
     ref.check(y, wy, depth, "y")
 
 
+@pytest.mark.parametrize("D", [1160, 2056, 2568, 3592, 4616, 6664, 8208, 10248, 12296, 14344])
+def test_layer_norm_of_ragged_widths(D):
+    # every split of a row over threads, its last vectors missing
+    B, L, nv = 2, 75, 70
+    x, dy = act(B, L, D, BF, D), act(B, L, D, BF, D + 1, outliers=False)
+    sc, sh = vec((B, 2, D), 0, 0.5, BF, 3), vec((B, 2, D), 0, 0.5, BF, 4)
+    y, mean, rstd = api.layer_norm(x, scale=sc, shift=sh, n_video=nv, eps=EPS)
+    want, wm, wr = ref.layer_norm(x, None, None, sc, sh, nv, EPS)
+    for got, w, what in ((y, want, "y"), (mean, wm, "mean"), (rstd, wr, "rstd")):
+        ref.check(got, w, ref.depth_row(D), what)
+    got = api.layer_norm_backward(dy, x, mean, rstd, scale=sc, n_video=nv)
+    want = ref.norm_backward(dy, x, mean, rstd, None, None, sc, None, nv, EPS, False)
+    ref.check(got.dx, want["dx"], ref.depth_row(D), "dx")
+    ref.check(got.dscale, want["dscale"], ref.depth_rows(B * L), "dscale")
+    ref.check(got.dshift, want["dshift"], ref.depth_rows(B * L), "dshift")
+
+
 def test_layer_norm_of_a_row_far_from_zero():
     # spread 1 about a mean of 4096: mean(x^2) - mean^2 would lose it in fp32
     x = act(2, 5, 1024, F32, 9, outliers=False, offset=4096.0)

@@ -605,7 +605,8 @@ size_t sol_dropout_backward_workspace_bytes(int64_t B, int64_t L, int64_t D);
  *
  * A plan (host memory, plain data; sol_rope_plan_init fills it) says how the
  * first rot_dim channels of a head are rotated: pair i turns by
- * pos[axis[i]] * freq[i].  A caller may overwrite freq (scaled ladders) with
+ * pos[axis[i]] * freq[i].  The other channels are left as they are, Inf and
+ * NaN among them.  A caller may overwrite freq (scaled ladders) with
  * any finite values.
  */
 typedef struct sol_rope_plan {

@@ -458,6 +458,94 @@ def test_rope_axes_far_positions():
                            api.rope_axes(q, None, small, plan)[0])
 
 
+# heads turned in part, the channels past rot_dim holding what arithmetic would spread:
+# rot_dim inside a lane's vector, at its end, one pair only, and several rounds of rows
+PARTIAL = [
+    # B, L, Hq, Hk, hd, sections, dtype, half, interleaved, per_axis, pos dtype
+    (1, 7, 3, 2, 16, (3,), BF, False, False, False, torch.int32),
+    (1, 33, 4, 3, 80, (1, 0, 11), BF, False, True, True, torch.int64),
+    (2, 19, 5, 1, 128, (10, 7), BF, False, True, False, torch.float32),
+    (2, 50, 2, 2, 96, (7, 20, 5), BF, True, False, True, torch.float32),
+    (1, 2401, 3, 2, 256, (32,), BF, True, False, False, torch.int32),
+    (1, 129, 2, 1, 128, (5,), F32, False, False, False, torch.int64),
+    (3, 700, 2, 1, 8, (1,), F32, False, False, False, torch.int32),
+    (2, 65, 3, 2, 40, (8, 4), F32, True, False, False, torch.float32),
+]
+
+
+def _spoil(x, rot, values):
+    """x with `values` in turn in one channel past rot_dim of every other head vector (each
+    channel's neighbours stay finite), everything else as it was."""
+    x = x.clone()
+    B, L, H, hd = x.shape
+    i = torch.arange(B * L * H, device=DEV)
+    col = rot + i // 2 % (hd - rot)
+    v = torch.tensor(values, device=DEV, dtype=x.dtype)[i % len(values)]
+    flat = x.view(-1, hd)
+    flat[i[::2], col[::2]] = v[::2]
+    return x
+
+
+def _bits(t):
+    return t.view(torch.int16 if t.dtype == BF else torch.int32)
+
+
+def _check_with_bad(got, want, depth, what):
+    """ref.check where the exact value is finite; the same Inf or NaN where not."""
+    value, mag = want
+    bad = ~torch.isfinite(value)
+    assert torch.equal(torch.isnan(got), torch.isnan(value)), f"{what}: NaN elsewhere"
+    inf = torch.isinf(value)
+    assert torch.equal(got[inf].double(), value[inf]), f"{what}: Inf elsewhere"
+    z = lambda t: torch.where(bad, torch.zeros((), dtype=t.dtype, device=DEV), t)  # noqa: E731
+    ref.check(z(got), (z(value), z(mag)), depth, what)
+
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.mark.parametrize("c", PARTIAL, ids=ids)
+def test_rope_axes_leaves_unrotated_channels_as_they_are(c):
+    pos, q, k, dq, dk, plan, pairs, half, _, _ = _rope_case(c)
+    rot = 2 * len(pairs)
+    for a, b, call in ((q, k, lambda a, b: api.rope_axes(a, b, pos, plan)),
+                       (dq, dk, lambda a, b: api.rope_axes_backward(a, b, pos, plan)[:2])):
+        clean = call(a, b)
+        sa, sb = (_spoil(t, rot, (INF, NAN, -INF, -0.0)) for t in (a, b))
+        for got, want, src in zip(call(sa, sb), clean, (sa, sb)):
+            assert torch.equal(_bits(got[..., rot:]), _bits(src[..., rot:]))
+            assert torch.equal(_bits(got[..., :rot]), _bits(want[..., :rot]))
+
+
+@pytest.mark.parametrize("c", PARTIAL, ids=ids)
+def test_rope_axes_with_the_norm_and_bad_unrotated_channels(c):
+    pos, q, k, dq, dk, plan, pairs, half, gq, gk = _rope_case(c)
+    B, L, Hq, Hk = c[:4]
+    rot = 2 * len(pairs)
+    args = dict(qk_norm=True, eps=EPS)
+    # the forward pass: an Inf makes its head's norm 0 and itself NaN
+    for bad in (INF, NAN):
+        sq, sk = _spoil(q, rot, (bad,)), _spoil(k, rot, (bad,))
+        for got, x, gm in zip(api.rope_axes(sq, sk, pos, plan, gq, gk, **args), (sq, sk), (gq, gk)):
+            _check_with_bad(got, ref.rope(x, pos, pairs, half, True, gm, EPS), 32, "out")
+    # a bad weight of one unrotated channel stays there
+    hq, hk = gq.clone(), gk.clone()
+    hq[rot], hk[-1] = INF, NAN
+    for got, x, gm in zip(api.rope_axes(q, k, pos, plan, hq, hk, **args), (q, k), (hq, hk)):
+        _check_with_bad(got, ref.rope(x, pos, pairs, half, True, gm, EPS), 32, "out")
+    # the gradient: bad incoming gradients of one channel reach that channel's dgamma
+    # alone, and dx through the head's mean
+    for bad in (INF, NAN):
+        sq, sk = dq.clone(), dk.clone()
+        sq[:, ::2, :, rot], sk[:, ::3, :, -1] = bad, bad
+        r = api.rope_axes_backward(sq, sk, pos, plan, q, k, gq, gk, **args)
+        for got, dgot, d, x, gm, H in ((r.dq, r.dgamma_q, sq, q, gq, Hq),
+                                       (r.dk, r.dgamma_k, sk, k, gk, Hk)):
+            dx, dg = ref.rope_backward(d, x, pos, pairs, half, True, gm, EPS)
+            _check_with_bad(got, dx, 48, "dx")
+            _check_with_bad(dgot, dg, ref.depth_rows(B * L * H), "dgamma")
+
+
 # ---------------------------------------------------------------------------
 # streams, graphs, a block
 # ---------------------------------------------------------------------------

@@ -6,7 +6,9 @@
 //             dx = rstd * (gamma g - x^ mean(x^ gamma g)),  x^ = x * rstd,
 //             dgamma = sum over rows and heads of g * x^
 // where R(pos) turns pair i of the first rot_dim channels by the angle
-// pos[axis_i] * freq_i and leaves the rest as they are.
+// pos[axis_i] * freq_i and leaves the rest as they are: copied bit for bit without
+// the norm, multiplied by nothing but rstd * gamma with it.  (A turn by 0 is not
+// that: Inf * 0 is NaN, and would reach the channel's neighbour too.)
 //
 // A warp owns a token row, as long as there is one for every warp of the grid;
 // the rows left after the last whole round are shared by WR warps each, so the
@@ -52,6 +54,11 @@ __device__ __forceinline__ uint4 ld_head16(const void *p) {
   return v;
 }
 
+__device__ __forceinline__ float2 and2(float2 v, uint32_t x, uint32_t y) {
+  return make_float2(__uint_as_float(__float_as_uint(v.x) & x),
+                     __uint_as_float(__float_as_uint(v.y) & y));
+}
+
 // cos and sin of pos * freq.  (Reduced to a part of a turn and sincospif: 3 to
 // 11% slower in calls of few rows, which wait for the angles.)
 __device__ __forceinline__ float2 cos_sin(double pos, double freq) {
@@ -81,8 +88,11 @@ constexpr int kRopeDepth = MODE == kNormRotateBack ? 2 : 4;
 constexpr int kRopeEntry = 4;
 
 // MODE as RopeMode.  HALF: pair i = channels (i, i + rot_dim / 2), else
-// (2i, 2i + 1).  The rows from whole_rows on are shared by 2^tail_log2 warps.
-template <typename T, int G, bool HALF, int MODE, int D>
+// (2i, 2i + 1).  PART: rot_dim < head_dim; a form of its own, as full rotations
+// need no masks (5 s clip, 96 of 128 channels turned, with masks / turned by 0
+// instead: forward with the norm 0.878 / 0.837 ms, half-split 0.902 / 0.874; its
+// gradient and the forms without the norm take the same time).  The rows from whole_rows on are shared by 2^tail_log2 warps.
+template <typename T, int G, bool HALF, int MODE, bool PART, int D>
 __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
     rope_axes_kernel(const __grid_constant__ RopeArgs a, int whole_rows, int tail_log2) {
   using IO = Io<T>;
@@ -125,6 +135,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
     col = turns ? (second ? e0 - half : e0) : 0;
     if (turns) partner = second ? lane - half / E : lane + half / E;
   }
+  // PART: all ones for the pairs that are turned (half-split: for the vector), 0 for
+  // the others, whose cross terms are masked away
+  uint32_t keep[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) keep[i] = (HALF ? turns : gl * P + i < half) ? 0xffffffffu : 0u;
 
   // frequency and position array of the pairs this lane computes
   double freq[NPL];
@@ -151,7 +166,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
     }
   };
   // identity entries past rot_dim are written once
-  if constexpr (!HALF) {
+  if constexpr (!HALF && PART) {
     for (int p = half + lane; p < PITCH; p += 32) {
       cosw[p] = 1.f;
       sinw[p] = 0.f;
@@ -279,6 +294,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
             A[m] = BACK ? c[m] : mul2(c[m], gam[m]);
             B[m] = mul2(s[m], splat2(sg));
             if constexpr (!BACK) B[m] = mul2(B[m], gp[m]);
+            if constexpr (PART) B[m] = and2(B[m], keep[0], keep[0]);  // gp may be Inf
           }
         } else {
           // entry m: pairs 2m and 2m + 1 of the lane; first P/2 entries of A, B for
@@ -297,6 +313,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
               B[m] = mul2(mul2(s[m], go), splat2(-1.f));          // even from odd
               A[m + P / 2] = mul2(c[m], go);                      // odd from odd
               B[m + P / 2] = mul2(s[m], ge);                      // odd from even
+              if constexpr (PART) {  // ge and go may be Inf
+                B[m] = and2(B[m], keep[2 * m], keep[2 * m + 1]);
+                B[m + P / 2] = and2(B[m + P / 2], keep[2 * m], keep[2 * m + 1]);
+              }
             }
             gam[2 * m] = ge;  // kept in the same split as the channels
             gam[2 * m + 1] = go;
@@ -314,6 +334,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
             vp.y = __shfl_sync(0xffffffffu, v.y, partner);
             vp.z = __shfl_sync(0xffffffffu, v.z, partner);
             vp.w = __shfl_sync(0xffffffffu, v.w, partner);
+            if constexpr (PART && NORM)
+              vp = make_uint4(vp.x & keep[0], vp.y & keep[0], vp.z & keep[0], vp.w & keep[0]);
             float2 own[P], oth[P];
             IO::unpack(v, own);
             IO::unpack(vp, oth);
@@ -324,13 +346,18 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
             IO::unpack_eo(v, ev, od);
 #pragma unroll
             for (int m = 0; m < P / 2; ++m) {
+              float2 ex = ev[m], ox = od[m];  // what crosses over to the other component
+              if constexpr (PART && NORM) {
+                ex = and2(ex, keep[2 * m], keep[2 * m + 1]);
+                ox = and2(ox, keep[2 * m], keep[2 * m + 1]);
+              }
               if constexpr (BACK) {
                 const float2 neg = mul2(B[m], splat2(-1.f));
-                o[2 * m] = fma2(ev[m], A[m], mul2(od[m], B[m]));
-                o[2 * m + 1] = fma2(od[m], A[m], mul2(ev[m], neg));
+                o[2 * m] = fma2(ev[m], A[m], mul2(ox, B[m]));
+                o[2 * m + 1] = fma2(od[m], A[m], mul2(ex, neg));
               } else {
-                o[2 * m] = fma2(ev[m], A[m], mul2(od[m], B[m]));
-                o[2 * m + 1] = fma2(od[m], A[m + P / 2], mul2(ev[m], B[m + P / 2]));
+                o[2 * m] = fma2(ev[m], A[m], mul2(ox, B[m]));
+                o[2 * m + 1] = fma2(od[m], A[m + P / 2], mul2(ex, B[m + P / 2]));
               }
             }
           }
@@ -390,6 +417,15 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
                 od[m] = o[2 * m + 1];
               }
               res = IO::pack_eo(ev, od);
+            }
+            if constexpr (PART && !NORM) {
+              // the words of unturned channels as they were read; a pair is one
+              // 32-bit word in bf16, two in fp32
+              constexpr int W = sizeof(T) / 2;  // words of a pair
+              res.x = keep[0] ? res.x : v.x;
+              res.y = keep[1 / W] ? res.y : v.y;
+              res.z = keep[2 / W] ? res.z : v.z;
+              res.w = keep[3 / W] ? res.w : v.w;
             }
             st_stream16(dst, res);
           }
@@ -469,12 +505,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
   }
 }
 
-template <typename T, int G, bool HALF, int MODE>
+template <typename T, int G, bool HALF, int MODE, bool PART>
 cudaError_t launch_t(RopeArgs &a, cudaStream_t stream, int *ctas) {
   constexpr bool DGAMMA = MODE == kNormRotateBack;
   constexpr int D = kRopeDepth<MODE>;
   constexpr int GW = 32 / G, WARPS = kRopeThreads / 32;
-  auto *kern = &rope_axes_kernel<T, G, HALF, MODE, D>;
+  auto *kern = &rope_axes_kernel<T, G, HALF, MODE, PART, D>;
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidConfiguration;
   constexpr int PITCH = G * Io<T>::E / 2;
@@ -496,14 +532,20 @@ cudaError_t launch_t(RopeArgs &a, cudaStream_t stream, int *ctas) {
   return cudaGetLastError();
 }
 
+template <typename T, int G, bool HALF, int MODE>
+cudaError_t dispatch_part(RopeArgs &a, cudaStream_t stream, int *ctas) {
+  return a.rot_dim < a.head_dim ? launch_t<T, G, HALF, MODE, true>(a, stream, ctas)
+                                : launch_t<T, G, HALF, MODE, false>(a, stream, ctas);
+}
+
 template <typename T, bool HALF, int MODE>
 cudaError_t dispatch_lanes(RopeArgs &a, cudaStream_t stream, int *ctas) {
   const int lanes = a.head_dim / Io<T>::E;
-  if (lanes <= 2) return launch_t<T, 2, HALF, MODE>(a, stream, ctas);
-  if (lanes <= 4) return launch_t<T, 4, HALF, MODE>(a, stream, ctas);
-  if (lanes <= 8) return launch_t<T, 8, HALF, MODE>(a, stream, ctas);
-  if (lanes <= 16) return launch_t<T, 16, HALF, MODE>(a, stream, ctas);
-  if (lanes <= 32) return launch_t<T, 32, HALF, MODE>(a, stream, ctas);
+  if (lanes <= 2) return dispatch_part<T, 2, HALF, MODE>(a, stream, ctas);
+  if (lanes <= 4) return dispatch_part<T, 4, HALF, MODE>(a, stream, ctas);
+  if (lanes <= 8) return dispatch_part<T, 8, HALF, MODE>(a, stream, ctas);
+  if (lanes <= 16) return dispatch_part<T, 16, HALF, MODE>(a, stream, ctas);
+  if (lanes <= 32) return dispatch_part<T, 32, HALF, MODE>(a, stream, ctas);
   return cudaErrorInvalidValue;
 }
 

@@ -655,7 +655,10 @@ typedef struct sol_positions {
 /* Head vectors: channel c of head h of row r of sample b is element
  * b*stride_b + r*stride_row + h*stride_head + c.  Strides are >= 0 and, like
  * data, multiples of 16 bytes.  An output's address distinct elements: in
- * order of their strides, each of its axes steps over all below it. */
+ * order of their strides, each of its axes steps over all below it.  Arrays may
+ * lie in each other's gaps (slices of one tensor); what counts as overlap is a
+ * shared byte.  (Two whose strides differ and are nested in neither order may
+ * take too long to tell apart and are then refused as overlapping.) */
 typedef struct sol_heads {
     void *data;         /* device */
     int64_t n_heads;    /* 1 .. 1024 */

@@ -420,6 +420,43 @@ def test_rope_axes_strides_and_shared_positions():
     assert torch.equal(qkv[..., 2 * H * hd:], v)
 
 
+@pytest.mark.parametrize("shape,perm,sl", [
+    # q and k as slices of one tensor, and where b, r, h, c of its axes are
+    ((2, 7, 45, 64), (0, 2, 1, 3), "heads"),          # [B, Hq + Hk, L, hd]
+    ((2, 3, 5, 45, 64), (0, 2, 1, 3), "axis"),        # [B, 3, H, L, hd]
+    ((2, 45, 5, 3, 64), (0, 1, 2, 3), "last"),        # [B, L, H, 3, hd]
+])
+@pytest.mark.parametrize("norm", [False, True])
+def test_rope_axes_in_place_on_slices_of_one_tensor(shape, perm, sl, norm):
+    g = torch.Generator(device=DEV).manual_seed(11)
+    buf = torch.randn(shape, generator=g, device=DEV).to(BF)
+    cut = {"heads": lambda t: (t[:, :5], t[:, 5:]), "axis": lambda t: (t[:, 0], t[:, 1]),
+           "last": lambda t: (t[..., 0, :], t[..., 1, :])}[sl]
+    heads = lambda t: [v.permute(perm) for v in cut(t)]  # noqa: E731
+    pos = torch.randint(0, 999, (3, 45), generator=g, device=DEV, dtype=torch.int32)
+    plan = api.RopeAxes(64, (8, 12, 12), half_split=True)
+    gam = [vec((64,), 1, 0.1, BF, i) if norm else None for i in (5, 6)]
+    q, k = heads(buf)
+    want = api.rope_axes(q.contiguous(), k.contiguous(), pos, plan, *gam, qk_norm=norm)
+    # two outputs in one tensor, then in place
+    out = torch.full(shape, 7.0, dtype=BF, device=DEV)
+    oq, ok = heads(out)
+    api.rope_axes(q, k, pos, plan, *gam, qk_norm=norm, q_out=oq, k_out=ok)
+    assert torch.equal(oq, want[0]) and torch.equal(ok, want[1])
+    if sl != "heads":
+        v = out[:, 2] if sl == "axis" else out[..., 2, :]
+        assert torch.all(v == 7.0)
+    api.rope_axes(q, k, pos, plan, *gam, qk_norm=norm, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    # the gradient, over the outputs' gradients
+    x = heads(torch.randn(shape, generator=g, device=DEV).to(BF)) if norm else (None, None)
+    ref_r = api.rope_axes_backward(q.contiguous(), k.contiguous(), pos, plan, *x, *gam,
+                                   qk_norm=norm)
+    r = api.rope_axes_backward(q, k, pos, plan, *x, *gam, qk_norm=norm, dq=q, dk=k)
+    for a, b in zip(r, ref_r):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
 def test_rope_axes_matches_the_grid_entry_point():
     # the implicit T x H x W grid written out as position ids
     w = WORKLOADS["tiny"]

@@ -2,6 +2,7 @@
 generator vectors, derivatives from differences), the plan, and the calls that
 the C ABI and the tensor wrappers refuse (fake, never-dereferenced addresses)."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -334,6 +335,124 @@ def test_rope_empty_and_reordered_axes_are_not_refused():
 def test_rope_backward_refused(kw, status):
     assert rope_bwd(**kw) == status
     assert _abi.last_error()
+
+
+# Arrays that lie in each other's gaps share no byte.  Nothing is launched: dgamma_q is
+# given gamma_q's address, which is refused once every heads array has passed.
+
+def _lay(shape, order, pick=None):
+    """Strides (b, row, head) and offset of a [B, L, H, hd] view of a tensor whose axes
+    lie in memory in `order` ('b', 'r', 'h', 'c', and 's' for slices, of which `pick`
+    is taken)."""
+    step, s, n = {}, 1, dict(shape)
+    for ax in reversed(order):
+        step[ax] = s
+        s *= n[ax]
+    return step["b"], step["r"], step["h"], (pick or 0) * step.get("s", 0)
+
+
+def _in_gaps(q, k, B, L, hd, over=None):
+    """Status and message of the gradient in place over dq_out = q's and dk_out = k's
+    layout, (stride_b, stride_row, stride_head, offset, heads) each; `over`: dk_out is
+    written over other heads than its own."""
+    at = lambda v, base=A: H(base + 2 * v[3], v[4], *v[:3])  # noqa: E731
+    st = rope_bwd(pl=plan(hd, (hd // 2,)), pos=P(sa=0, sb=0), dqo=at(q), dko=at(k),
+                  q=at(q, A + 2 * G), k=at(k, A + 2 * G), dq=at(q), dk=at(over or k), B=B, L=L,
+                  dgq=A + 8 * G)
+    return st, _abi.last_error()
+
+
+@pytest.mark.parametrize("B", [1, 2, 5])
+@pytest.mark.parametrize("L", [1, 7, 300])
+@pytest.mark.parametrize("Hq,Hk", [(3, 3), (4, 1), (1, 2), (1, 1)])
+def test_rope_takes_slices_of_one_tensor(B, L, Hq, Hk):
+    hd, n = 64, dict(b=B, r=L, h=Hq + Hk, c=64)
+    layouts = []
+    # q and k as heads of one buffer, [B, Hq + Hk, L, hd] and the other orders
+    for order in ("bhrc", "brhc", "hbrc", "rbhc", "hrbc", "rhbc"):
+        sb, sr, sh, _ = _lay(n, order)
+        layouts.append(((sb, sr, sh, 0, Hq), (sb, sr, sh, Hq * sh, Hk)))
+    if Hq == Hk:      # q, k, v as slices: [B, 3, H, L, hd], [B, L, H, 3, hd] and others
+        n = dict(b=B, r=L, h=Hq, c=64, s=3)
+        for order in ("bshrc", "brhsc", "sbrhc", "bhsrc", "brshc", "rbshc", "bhrsc"):
+            for i, j in ((0, 1), (1, 0), (0, 2)):
+                layouts.append(tuple((*_lay(n, order, p), Hq) for p in (i, j)))
+    for q, k in layouts:
+        st, msg = _in_gaps(q, k, B, L, hd)
+        assert st == INV and "dgamma_q overlaps gamma_q" in msg, (q, k, msg)
+        # one vector off, the outputs meet
+        if (B, L, Hq + Hk) != (1, 1, 2):
+            st, msg = _in_gaps(q, k, B, L, hd, over=(*q[:3], q[3] + 8, Hk))
+            assert st == INV and "dgamma" not in msg, (q, k, msg)
+
+
+def _touched(v, B, L, hd):
+    """The 16-byte units of a heads array (bf16, offsets and strides in elements)."""
+    sb, sr, sh, off, n = v
+    return {(off + b * sb + r * sr + h * sh) // 8 + c for b in range(B) for r in range(L)
+            for h in range(n) for c in range(hd // 8)}
+
+
+def _nested(v, B, L, hd):
+    """Whether each axis steps over all below it, as an output's must."""
+    extent = hd
+    for step, n in sorted(zip(v[:3], (B, L, v[4]))):
+        if n > 1:
+            if step < extent:
+                return False
+            extent += (n - 1) * step
+    return True
+
+
+def test_rope_overlap_of_random_layouts_is_exact():
+    rng = random.Random(5)
+    seen = {True: 0, False: 0}
+    for _ in range(4000):
+        B, L, hd = rng.randint(1, 3), rng.randint(1, 4), 8 * rng.randint(1, 2)
+        two = []
+        for _ in "qk":
+            n = rng.randint(1, 3)
+            # nested strides in any order with gaps, in units of 8 elements
+            axes, step, s = [("b", B), ("r", L), ("h", n)], {}, hd // 8
+            rng.shuffle(axes)
+            for ax, count in axes:
+                s += rng.choice((0, 0, 0, 1, 2, 5))
+                step[ax] = 8 * s
+                s *= count
+            two.append((step["b"], step["r"], step["h"], 8 * rng.randint(0, 30), n))
+        if rng.random() < 0.5:        # slices of one tensor have the same strides
+            two[1] = (*two[0][:3], *two[1][3:])
+        q, k = two
+        units = [_touched(v, B, L, hd) for v in two]
+        if not all(_nested(v, B, L, hd) for v in two):
+            continue                  # k's heads under q's strides: refused as such
+        st, msg = _in_gaps(q, k, B, L, hd)
+        apart = not units[0] & units[1]
+        assert st == INV and ("dgamma_q overlaps gamma_q" in msg) == apart, (two, B, L, hd, msg)
+        seen[apart] += 1
+    assert min(seen.values()) > 300
+
+
+def test_rope_small_arrays_in_the_gaps_of_heads():
+    # gamma_q, positions and dgamma_k between the heads of dq's rows
+    wide = H(A + 4 * G, sr=1024, sb=4096)        # 256 of 1,024 elements a row
+    gap = A + 4 * G + 600
+    for kw in (dict(gq=gap + 8, dgq=gap + 8), dict(pos=P(gap + 8, sa=0, sb=0), dgq=A + 8 * G),
+               dict(dgk=gap + 8, dgq=A + 8 * G)):
+        assert rope_bwd(dq=wide, **kw) == INV
+        assert "dgamma_q overlaps gamma_q" in _abi.last_error(), kw
+    for kw in (dict(gq=A + 4 * G + 496), dict(pos=P(A + 4 * G + 508, sa=0, sb=0)),
+               dict(dgk=A + 4 * G + 2048)):
+        assert rope_bwd(dq=wide, **kw) == INV
+        assert "output overlaps" in _abi.last_error(), kw
+
+
+def test_rope_layouts_that_cannot_be_told_apart_in_time_are_refused():
+    # steps that nest in nothing: the check gives up, it does not hang
+    q = (2 ** 19 + 8, 2 ** 19, 2 ** 19 + 16, 0, 1000)
+    k = (2 ** 19 + 24, 2 ** 19 + 32, 2 ** 19 + 40, 64, 1000)
+    st, msg = _in_gaps(q, k, 1000, 1000, 64)
+    assert st == INV and "overlap" in msg
 
 
 # ---------------------------------------------------------------------------

@@ -275,17 +275,88 @@ bool heads_separate(const sol_heads &h, int64_t B, int64_t L, int head_dim) {
   return true;
 }
 
-// True if the two share no byte: apart in memory, or column blocks of rows of
-// one pitch (q, k and v of a merged projection).
-bool heads_disjoint(const sol_heads &a, const sol_heads &b, int64_t B, int64_t L, int head_dim,
-                    int es) {
-  const Span sa = span_of(a.data, 1, 0, heads_extent(a, B, L, head_dim, es));
-  const Span sb = span_of(b.data, 1, 0, heads_extent(b, B, L, head_dim, es));
-  if (!spans_overlap(sa, sb)) return true;
-  int64_t ld = a.stride_row;
-  if (L == 1) ld = B > 1 ? a.stride_b : 0;
-  const int64_t ldb = L == 1 ? (B > 1 ? b.stride_b : 0) : b.stride_row;
-  if (ld <= 0 || ld != ldb) return false;
+// The bytes of a strided array: runs of `width` bytes at p plus any sum of t * step
+// with 0 <= t < count, one t per axis.
+struct Runs {
+  const void *p;
+  int64_t width;
+  std::pair<int64_t, int64_t> ax[3];  // (step, count)
+};
+Runs runs_of(const sol_heads &h, int64_t B, int64_t L, int head_dim, int es) {
+  // (the step of an axis of one element says nothing)
+  auto axis = [&](int64_t stride, int64_t n) {
+    return std::pair<int64_t, int64_t>(n > 1 ? stride * es : 0, n);
+  };
+  return {h.data, int64_t(head_dim) * es,
+          {axis(h.stride_b, B), axis(h.stride_row, L), axis(h.stride_head, h.n_heads)}};
+}
+Runs runs_of(const Arr &a) { return {a.p, a.bytes, {{0, 1}, {0, 1}, {0, 1}}}; }
+
+// True if no byte of `a` is one of `b`.  They meet where the distance between two
+// runs, b.p - a.p + sum t * step (t >= 0 for b's axes, <= 0 for a's), lies in
+// (-b.width, a.width).  Axes of one step count as one; from the largest step down,
+// only the t from which the smaller steps still reach that interval are followed: two
+// or three per axis where the steps nest, as in any layout of a tensor or of slices of
+// one.  Layouts that take more than kMeetSteps to tell apart count as meeting.
+constexpr int kMeetSteps = 1 << 14;
+class Distance {
+ public:
+  Distance(const Runs &a, const Runs &b) : wa_(a.width), wb_(b.width) {
+    off_ = static_cast<__int128>(reinterpret_cast<intptr_t>(b.p)) -
+           reinterpret_cast<intptr_t>(a.p);
+    for (const auto &[step, count] : b.ax) add(step, 0, count - 1);
+    for (const auto &[step, count] : a.ax) add(step, 1 - count, 0);
+    std::sort(term_, term_ + n_, [](const Term &x, const Term &y) { return x.step > y.step; });
+    for (int i = n_ - 1; i >= 0; --i) {
+      term_[i].least = term_[i].lo * term_[i].step + (i + 1 < n_ ? term_[i + 1].least : 0);
+      term_[i].most = term_[i].hi * term_[i].step + (i + 1 < n_ ? term_[i + 1].most : 0);
+    }
+  }
+  bool meets() { return meets_from(0, off_); }
+
+ private:
+  struct Term {
+    __int128 step, lo, hi;
+    __int128 least, most;  // of this term and all smaller ones
+  };
+  void add(int64_t step, int64_t lo, int64_t hi) {
+    if (step == 0 || lo == hi) return;
+    for (int i = 0; i < n_; ++i) {
+      if (term_[i].step != step) continue;
+      term_[i].lo += lo;
+      term_[i].hi += hi;
+      return;
+    }
+    term_[n_++] = Term{step, lo, hi, 0, 0};
+  }
+  static __int128 floor_div(__int128 x, __int128 y) {  // y > 0
+    return x / y - (x % y < 0 ? 1 : 0);
+  }
+  bool meets_from(int i, __int128 off) {
+    const __int128 least = i < n_ ? term_[i].least : 0, most = i < n_ ? term_[i].most : 0;
+    if (off + least >= wa_ || off + most <= -wb_) return false;
+    if (i == n_ || --left_ < 0) return true;
+    const Term &t = term_[i];
+    const __int128 rest_least = t.least - t.lo * t.step, rest_most = t.most - t.hi * t.step;
+    // t * step < wa - off - rest_least and t * step > -wb - off - rest_most
+    const __int128 first = std::max(t.lo, floor_div(-wb_ - off - rest_most, t.step) + 1);
+    const __int128 last = std::min(t.hi, floor_div(wa_ - off - rest_least - 1, t.step));
+    for (__int128 k = first; k <= last; ++k)
+      if (meets_from(i + 1, off + k * t.step)) return true;
+    return false;
+  }
+  __int128 wa_, wb_, off_;
+  Term term_[6];
+  int n_ = 0, left_ = kMeetSteps;
+};
+bool runs_disjoint(const Runs &a, const Runs &b) { return !Distance(a, b).meets(); }
+
+// True if a and b lie in column blocks of rows of one pitch (q, k and v of a merged
+// projection), whatever their samples' steps: said without following those.
+bool column_blocks(const sol_heads &a, const sol_heads &b, int64_t B, int64_t L, int head_dim,
+                   int es) {
+  const int64_t ld = a.stride_row;
+  if (L == 1 || ld <= 0 || ld != b.stride_row) return false;
   if (B > 1 && (a.stride_b % ld != 0 || b.stride_b % ld != 0)) return false;
   const int64_t wa = ((a.n_heads - 1) * a.stride_head + head_dim) * es;
   const int64_t wb = ((b.n_heads - 1) * b.stride_head + head_dim) * es;
@@ -294,6 +365,13 @@ bool heads_disjoint(const sol_heads &a, const sol_heads &b, int64_t B, int64_t L
               (ld * es);
   if (c < 0) c += ld * es;
   return wa <= c && c + wb <= ld * es;
+}
+
+// True if the two share no byte.
+bool heads_disjoint(const sol_heads &a, const sol_heads &b, int64_t B, int64_t L, int head_dim,
+                    int es) {
+  return column_blocks(a, b, B, L, head_dim, es) ||
+         runs_disjoint(runs_of(a, B, L, head_dim, es), runs_of(b, B, L, head_dim, es));
 }
 
 HeadsArg heads_arg(const sol_heads *h, int es) {
@@ -374,12 +452,12 @@ sol_status rope_args(const char *fn, const sol_rope_plan *plan, const sol_positi
                        {"gamma_k", gamma_k, static_cast<int64_t>(hd) * es}};
   for (int t = 0; t < 2; ++t) {
     if (!out[t]) continue;
-    const Span so = span_of(out[t]->data, 1, 0, heads_extent(*out[t], B, L, hd, es));
+    const Runs ro = runs_of(*out[t], B, L, hd, es);
     for (const Arr &s : small)
-      if (s.p && spans_overlap(so, span_of(s.p, 1, 0, s.bytes)))
+      if (s.p && !runs_disjoint(ro, runs_of(s)))
         return fail(SOL_ERR_INVALID_ARG, "%s: an output overlaps %s", fn, s.name);
     for (const Arr &o : other_outs)
-      if (o.p && o.bytes && spans_overlap(so, span_of(o.p, 1, 0, o.bytes)))
+      if (o.p && o.bytes && !runs_disjoint(ro, runs_of(o)))
         return fail(SOL_ERR_INVALID_ARG, "%s: an output overlaps %s", fn, o.name);
     for (int u = 0; u < 2; ++u)
       for (const sol_heads *h : {x[u], g[u]}) {
@@ -402,7 +480,7 @@ sol_status rope_args(const char *fn, const sol_rope_plan *plan, const sol_positi
         return fail(SOL_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, o.name, q.name);
     for (int u = 0; u < 2; ++u)
       for (const sol_heads *h : {x[u], g[u]})
-        if (h && spans_overlap(so, span_of(h->data, 1, 0, heads_extent(*h, B, L, hd, es))))
+        if (h && !runs_disjoint(runs_of(o), runs_of(*h, B, L, hd, es)))
           return fail(SOL_ERR_INVALID_ARG, "%s: %s overlaps an input", fn, o.name);
   }
 

@@ -549,7 +549,9 @@ size_t sol_norm_backward_workspace_bytes(int64_t B, int64_t L, int64_t D);
  * at counter (e / 4, offset + site), key seed, both 64-bit words low half
  * first, is at least round(p * 2^32).  The mask is a function of (seed,
  * offset + site, e, p) and is never stored: the backward call computes it
- * again.  A dropped element adds 0 whatever branch holds there.
+ * again.  A dropped element adds 0 whatever branch holds there.  Elements
+ * are numbered from 0 in every call: ranks, and calls on parts of a batch, drop
+ * the same ones unless each has a seed of its own.
  *
  *   h             [B, L, D] device, or NULL for 0.
  *   branch        [B, L, D] device.
@@ -559,7 +561,10 @@ size_t sol_norm_backward_workspace_bytes(int64_t B, int64_t L, int64_t D);
  *                 kernel, so that a captured graph draws another mask when its
  *                 owner changes them between replays.  May be NULL if p = 0.
  *   site          added to offset (modulo 2^64): one number per dropout of a
- *                 step keeps their masks apart.
+ *                 step, 0 .. sites - 1, keeps their masks apart.  The counter
+ *                 holds the sum, so a step must move offset by at least the
+ *                 number of its sites: (offset + 1, site) is the mask of
+ *                 (offset, site + 1).
  *   p             0 <= p <= 1 (p = 0 keeps all: sol_gate_residual; p = 1 drops
  *                 all).
  *   n_video, D    as for sol_rms_adaln (same D limit).

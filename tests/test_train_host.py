@@ -2,7 +2,9 @@
 generator vectors, derivatives from differences), the plan, and the calls that
 the C ABI and the tensor wrappers refuse (fake, never-dereferenced addresses)."""
 import ctypes
+import pathlib
 import random
+import re
 
 import pytest
 import torch
@@ -44,6 +46,22 @@ def test_mask_reference_places_the_words():
         ctr = [e // 4 & 0xFFFFFFFF, e // 4 >> 32, offset & 0xFFFFFFFF, offset >> 32]
         w = ref.philox(ctr, [seed & 0xFFFFFFFF, seed >> 32])[e % 4]
         assert bool(got[i]) == (w >= round(p * 2 ** 32))
+
+
+def test_readme_recipe_draws_a_mask_of_its_own_for_every_step_and_layer():
+    # the counter holds offset + site: steps and sites must not add up to the same
+    text = (pathlib.Path(__file__).parent.parent / "README.md").read_text()
+    rng_of = re.search(r"^rng = (torch\.tensor\(.*\))  +#", text, re.M).group(1)
+    sites = set(re.findall(r"rng, site=(.*)\)", text))
+    assert len(sites) == 1            # the gradient's is the forward call's
+    masks, n_layers = set(), 5
+    for step in range(4):
+        for layer in range(n_layers):
+            env = dict(torch=torch, seed=7, step=step, layer=layer, n_layers=n_layers)
+            seed, offset = eval(rng_of.replace('"cuda"', '"cpu"'), env).tolist()
+            keep = ref.keep_mask(512, seed, offset + eval(min(sites), env), 0.5, "cpu")
+            masks.add(bytes(keep.numpy()))
+    assert len(masks) == 4 * n_layers
 
 
 def _scalars(seed, B=2, L=3, D=8):

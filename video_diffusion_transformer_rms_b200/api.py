@@ -527,7 +527,8 @@ def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], site: int = 
     tensor whose last dimension is one that layer_norm takes.  The mask is a
     function of (seed, offset + site, the element's index, p), with rng = (seed,
     offset) two int64 on x's device: the gradient is dropout(dout, p, rng,
-    site)."""
+    site).  Every step moves offset by at least its number of sites, or masks come
+    again; ranks and parts of a batch need seeds of their own."""
     if x.dim() < 1 or not x.is_contiguous():
         raise ValueError("x must be a contiguous tensor")
     po = _arg(out, x.shape, "out", x)

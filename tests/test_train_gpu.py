@@ -13,6 +13,7 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda"
 BF, F32 = torch.bfloat16, torch.float32
 EPS = 1e-6
+INF, NAN = float("inf"), float("nan")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -86,6 +87,74 @@ def test_layer_norm_of_ragged_widths(D):
     ref.check(got.dx, want["dx"], ref.depth_row(D), "dx")
     ref.check(got.dscale, want["dscale"], ref.depth_rows(B * L), "dscale")
     ref.check(got.dshift, want["dshift"], ref.depth_rows(B * L), "dshift")
+
+
+@pytest.mark.parametrize("D,dt", [(1024, BF), (1016, BF), (8192, BF), (8184, BF), (512, F32),
+                                  (4096, F32), (6144, BF)])
+def test_layer_norm_of_full_and_almost_full_widths(D, dt):
+    # 32 x 4 and 256 x 4 vectors, filled and one vector short; 1536 vectors do for three
+    # vectors per thread in the gradients
+    B, L, nv = 2, 75, 70
+    x, dy = act(B, L, D, dt, D), act(B, L, D, dt, D + 1, outliers=False)
+    g, b = vec((D,), 1, 0.1, dt, 1), vec((D,), 0, 0.3, dt, 2)
+    sc, sh = vec((B, 2, D), 0, 0.5, dt, 3), vec((B, 2, D), 0, 0.5, dt, 4)
+    y, mean, rstd = api.layer_norm(x, g, b, sc, sh, n_video=nv, eps=EPS)
+    want, wm, wr = ref.layer_norm(x, g, b, sc, sh, nv, EPS)
+    for got, w, what in ((y, want, "y"), (mean, wm, "mean"), (rstd, wr, "rstd")):
+        ref.check(got, w, ref.depth_row(D), what)
+    for dres in (None, act(B, L, D, dt, D + 2)):
+        t = dict(x=x, dy=dy, gamma=g, beta=b, scale=sc, dres=dres)
+        got = api.layer_norm_backward(dy, x, mean, rstd, g, b, sc, n_video=nv, dres=dres)
+        want = ref.norm_backward(dy, x, mean, rstd, g, b, sc, dres, nv, EPS, False)
+        _check_norm_grads(got._asdict(), want, (B, L, nv, D, dt), t)
+
+
+# every count of vectors per thread of the gradients, full (an instantiation without
+# guards in the RMS form) and ragged
+@pytest.mark.parametrize("D,dt", [(256, BF), (248, BF), (1024, BF), (2056, BF), (5120, BF),
+                                  (5128, BF), (6144, BF), (10248, BF), (12288, BF), (12296, BF),
+                                  (14344, BF), (16384, BF), (16376, BF), (6148, F32), (8192, F32)])
+@pytest.mark.parametrize("dres", [False, True])
+def test_rms_adaln_backward_of_every_width(D, dt, dres):
+    case = (2, 75, 70, D, dt)
+    t, want = _norm_case(case, True, True, True, dres)
+    dx, dscale, dshift, dgamma = api.rms_adaln_backward(t["dy"], t["x"], t["scale"], 70,
+                                                        gamma=t["gamma"], eps=EPS,
+                                                        dres=t["dres"])
+    _check_norm_grads(dict(dx=dx, dscale=dscale, dshift=dshift, dgamma=dgamma), want, case, t)
+
+
+@pytest.mark.parametrize("D,dt", [(8, BF), (264, BF), (5120, BF), (5128, BF), (1000, F32),
+                                  (16384, BF)])
+def test_norms_keep_bad_rows_to_themselves(D, dt):
+    # an Inf or NaN in one element makes its row bad, and the channel's or the whole
+    # sums, but no other row, whatever shares its warp, ring or CTA
+    B, L, nv = 2, 61, 40
+    x, dy = act(B, L, D, dt, D), act(B, L, D, dt, D + 1, outliers=False)
+    sc, sh = vec((B, 2, D), 0, 0.5, dt, 3), vec((B, 2, D), 0, 0.5, dt, 4)
+    rows = [(0, 0), (0, 33), (0, L - 1), (1, 7)]
+    bx, bdy = x.clone(), dy.clone()
+    good = torch.ones((B, L), dtype=torch.bool, device=DEV)
+    for i, (b, r) in enumerate(rows):
+        bx[b, r, (5 * i) % D] = (INF, NAN, -INF, INF)[i]
+        bdy[b, (r + 3) % L, i % D] = (NAN, INF, INF, -INF)[i]
+        good[b, r] = good[b, (r + 3) % L] = False
+    fx = torch.isfinite(bx).all(-1)
+    clean = api.layer_norm(x, scale=sc, shift=sh, n_video=nv)
+    got = api.layer_norm(bx, scale=sc, shift=sh, n_video=nv)
+    for a, b in zip(got, clean):
+        assert torch.equal(a[fx], b[fx])
+    assert torch.isnan(got[0][~fx]).any(-1).all()
+    args = dict(scale=sc, n_video=nv)
+    a = api.layer_norm_backward(dy, x, clean[1], clean[2], **args).dx
+    b = api.layer_norm_backward(bdy, bx, *got[1:], **args).dx
+    assert torch.equal(a[good], b[good]) and not torch.isfinite(b[~good]).all(-1).any()
+    a = api.rms_adaln_backward(dy, x, sc, nv)[0]
+    b, _, dshift, _ = api.rms_adaln_backward(bdy, bx, sc, nv)
+    assert torch.equal(a[good], b[good]) and not torch.isfinite(b[~good]).all(-1).any()
+    # the sums of dy alone: bad in the channels that hold something bad, elsewhere not
+    want = ref.key_sums(bdy.double(), nv)
+    assert torch.equal(torch.isfinite(dshift), torch.isfinite(want))
 
 
 def test_layer_norm_of_a_row_far_from_zero():
@@ -536,9 +605,6 @@ def _check_with_bad(got, want, depth, what):
     assert torch.equal(got[inf].double(), value[inf]), f"{what}: Inf elsewhere"
     z = lambda t: torch.where(bad, torch.zeros((), dtype=t.dtype, device=DEV), t)  # noqa: E731
     ref.check(z(got), (z(value), z(mag)), depth, what)
-
-
-INF, NAN = float("inf"), float("nan")
 
 
 @pytest.mark.parametrize("c", PARTIAL, ids=ids)

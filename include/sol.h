@@ -594,6 +594,9 @@ sol_status sol_dropout_residual(const void *h, const void *branch,
  *   workspace     sol_dropout_backward_workspace_bytes; may be NULL if dgate
  *                 is.
  *   p = 0 gives the gradient of sol_gate_residual.
+ *
+ * dbranch is rounded in the order written: dout * (1 / (1 - p)) to fp32, its
+ * product with gate to fp32, that to the element type.
  */
 sol_status sol_dropout_residual_backward(
     const void *dout, const void *branch, const void *gate, void *dbranch,

@@ -330,6 +330,31 @@ def test_dropout_residual_backward(case, p):
         assert torch.equal(a, dbranch) and torch.equal(b, dgate)
 
 
+@pytest.mark.parametrize("case", ROWS, ids=ids)
+@pytest.mark.parametrize("p", [0.1, 0.25])
+def test_dropout_gradient_rounds_in_the_order_of_its_formula(case, p):
+    # gate * (dout / (1 - p)): the quotient is rounded to fp32, then the product, then the
+    # output.  Many of the exact results are ties of bf16 (p = 1/4: all whose factors have
+    # a 3), which another order rounds the other way.
+    B, L, nv, D, dt = case
+    do, br = act(B, L, D, dt, D, outliers=False), act(B, L, D, dt, D + 1)
+    gate = vec((B, 2, D), 0.0, 0.3, dt, 5)
+    rng = _rng()
+    keep = ref.keep_mask(do.numel(), RNG[0], RNG[1] + 3, ref.p32(p), DEV).view_as(do)
+    ks = torch.tensor(1.0 / (1.0 - ref.p32(p)), dtype=torch.float32, device=DEV)
+    want = ref.spread(gate, nv, L).float() * (do.float() * ks)
+    want = torch.where(keep, want, torch.zeros((), device=DEV)).to(dt)
+    dbranch, _ = api.dropout_residual_backward(do, br, gate, nv, p, rng, site=3)
+    assert torch.equal(dbranch, want)
+    # and where dgate is not wanted
+    other = torch.empty_like(do)
+    _abi.check(_abi.sol_dropout_residual_backward(
+        do.data_ptr(), None, gate.data_ptr(), other.data_ptr(), None, rng.data_ptr(), 3, p, B, L,
+        nv, D, None, 0, _abi.SOL_BF16 if dt == BF else _abi.SOL_F32,
+        torch.cuda.current_stream().cuda_stream))
+    assert torch.equal(other, want)
+
+
 def test_dropout_mask_is_a_function_of_seed_offset_and_element():
     x = torch.ones((1, 513, 520), device=DEV)
     a = api.dropout(x, 0.5, _rng(), site=1)

@@ -651,7 +651,10 @@ typedef enum sol_pos_type {
 
 /* Position ids: axis a of row r of sample b is element a*stride_axis +
  * b*stride_b + r.  stride_b = 0 shares one set of rows among the samples.
- * Angles are exact to fp32 for |position| up to 2^31. */
+ * Angles are pos * freq in 64 bits, off by at most |pos * freq| * 2^-53 for the
+ * freq in the plan, which sol_rope_plan_init rounds to within a few 2^-53 of
+ * itself: about 5e-7 rad at |position| = 2^31.  cos and sin have that error and
+ * their rounding to fp32. */
 typedef struct sol_positions {
     const void *data;   /* device, aligned to its element */
     int32_t type;       /* sol_pos_type */

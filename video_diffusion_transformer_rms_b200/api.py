@@ -2,6 +2,10 @@
 their pointers, shapes and the current stream to libsol.  Marshalling only
 (PyTorch allocates outputs when the caller does not pass them); the
 arithmetic runs in libsol's kernels.
+
+No call is recorded by autograd: a result does not require a gradient even where
+an input does, and nothing warns of it.  The gradients are the _backward calls;
+a caller that trains through autograd wraps the pairs in torch.autograd.Function.
 """
 import contextlib
 from typing import NamedTuple, Optional, Sequence, Tuple

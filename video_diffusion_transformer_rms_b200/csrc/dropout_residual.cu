@@ -34,9 +34,10 @@
 namespace sol {
 namespace {
 
-// 128 threads with up to 128 registers, 4 rows each: 0.627 ms for the forward
-// pass at the 5 s clip, 0.653 ms for the backward (256 x 128 registers: 0.655 and
-// 0.683; 256 x 80: 0.677 and 0.733).
+// 128 threads with up to 128 registers, 4 rows each: 0.623 ms for the forward
+// pass at the 5 s clip, 0.650 ms for the backward.  (Against 0.627 and 0.653 of an
+// earlier form, 256 threads x 128 registers took 0.655 and 0.683, x 80 0.677 and
+// 0.733.)
 constexpr int kDropThreads = 128;  // bound on NT * RG
 constexpr int kDropCtas = 4;       // CTAs per SM the registers are to leave room for
 // rows per thread and pass (fp32, 60,000 x 5120: three 0.564, four 0.588 ms; its
@@ -339,9 +340,9 @@ __global__ void __launch_bounds__(kDropThreads, kDropCtas)
   }
 }
 
-// Vectors of a row over `tiles` tiles of NT threads: the tile count of at
-// most 256 threads each that leaves the fewest threads idle, the wider tile
-// where they tie (640 vectors: 4 x 160).
+// Vectors of a row over `tiles` tiles of NT threads, at most kDropThreads: of the
+// four smallest tile counts the one that leaves the fewest threads idle, the wider
+// tile where they tie (640 vectors: 5 x 128).
 void pick_tiles(int nvec, int *tiles, int *nt) {
   const int t0 = (nvec + kDropThreads - 1) / kDropThreads;
   int best = -1;

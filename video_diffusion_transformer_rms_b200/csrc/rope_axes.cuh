@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeMinCtas<MODE>)
     if (passes_q + passes_k == 0) row = end;  // more warps than heads: none for this one
 
     // The ring's producer: it walks the same rows, tensors and passes as the loop
-    // below, D - 1 vectors ahead.
+    // below, D - 1 entries of up to RV heads ahead.
     int64_t prow = row;
     int pt = passes_q > 0 ? 0 : 1, phead = slot, pleft = 0, pslot = 0, cons = 0;
     const unsigned char *px = nullptr, *pg = nullptr;

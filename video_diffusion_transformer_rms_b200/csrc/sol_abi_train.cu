@@ -28,18 +28,18 @@ sol_status guarded(F &&body) {
 
 int dtype_index(sol_dtype dt) { return dt == SOL_F32 ? 0 : 1; }
 
-// An array of a call: its bytes, its name, and whether the call writes it.
-// `same` lists the inputs an output may equal exactly.
+// An array of a call.
 struct Arr {
   const char *name;
   const void *p;
   int64_t bytes;
 };
-// Every output overlaps no other argument, except those it may equal.
+// An output and an input that it may equal exactly.
 struct Alias {
   const void *out;
   const void *in;
 };
+// Every output overlaps no other argument, except those in `equal`.
 sol_status check_overlaps(const char *fn, std::initializer_list<Arr> ins,
                           std::initializer_list<Arr> outs, std::initializer_list<Alias> equal) {
   auto may = [&](const void *o, const void *i) {

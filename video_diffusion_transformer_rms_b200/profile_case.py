@@ -4,7 +4,8 @@ for profilers (ncu) that should capture a small, self-contained case.
     python -m video_diffusion_transformer_rms_b200.profile_case \
         [--workload clip5s] [--frames 4] [--launches 1]
         [--kernel norm|rms|gate|qk|qk_tab|gemm|qk_bhsd|qk_half|qk_int8|qk_all|next|
-                  train|ln|ln_bwd|rms_bwd|drop|drop_bwd|rope|rope_bwd] [--table]
+                  train|ln|ln_bwd|rms_bwd|drop|drop_bwd|rope|rope_bwd|
+                  rope_plain|rope_plain_bwd] [--table]
 
 The slice keeps the clip's H x W latent grid, D and head layout, takes the
 first `--frames` latent frames (T) and scales the audio rows by the same
@@ -20,8 +21,9 @@ RMS-AdaLN and the change detector (read-only, then with the cache refresh).
 `--kernel norm` runs the step's three kernels; `rms`, `gate`, `qk` (per-row
 cos/sin) and `qk_tab` (rotary table) one of them alone, for captures that
 must hold a single kernel.  `--kernel train` runs every training operator,
-`ln` .. `rope_bwd` one of them alone (layer norm with AdaLN modulation, dropout
-with p = 0.1, rotation at position ids behind QKNorm).  `--table` makes the qk_* variants read a rotary
+`ln` .. `rope_plain_bwd` one of them alone (layer norm with AdaLN modulation,
+dropout with p = 0.1, rotation at position ids behind QKNorm or, `rope_plain`,
+without it).  `--table` makes the qk_* variants read a rotary
 table too.  The slice prints its row count (the scale factor to the full
 workload's traffic).
 """
@@ -34,7 +36,8 @@ from . import _abi, api
 from .workloads import WORKLOADS, make_inputs
 
 
-TRAIN = ("ln", "ln_bwd", "rms_bwd", "drop", "drop_bwd", "rope", "rope_bwd")
+TRAIN = ("ln", "ln_bwd", "rms_bwd", "drop", "drop_bwd", "rope", "rope_bwd", "rope_plain",
+         "rope_plain_bwd")
 
 
 def main():
@@ -147,6 +150,8 @@ def train_case(w, which, launches):
         "rope": lambda: api.rope_axes(q, k, pos, plan, gq, gk, qk_norm=True, eps=w.eps),
         "rope_bwd": lambda: api.rope_axes_backward(dq, dk, pos, plan, q, k, gq, gk, qk_norm=True,
                                                    eps=w.eps),
+        "rope_plain": lambda: api.rope_axes(q, k, pos, plan),
+        "rope_plain_bwd": lambda: api.rope_axes_backward(dq, dk, pos, plan),
     }
     for _ in range(launches):
         for n in names:

@@ -280,6 +280,7 @@ bool heads_separate(const sol_heads &h, int64_t B, int64_t L, int head_dim) {
 struct Runs {
   const void *p;
   int64_t width;
+  int64_t extent;                     // from the first byte past the last
   std::pair<int64_t, int64_t> ax[3];  // (step, count)
 };
 Runs runs_of(const sol_heads &h, int64_t B, int64_t L, int head_dim, int es) {
@@ -287,10 +288,9 @@ Runs runs_of(const sol_heads &h, int64_t B, int64_t L, int head_dim, int es) {
   auto axis = [&](int64_t stride, int64_t n) {
     return std::pair<int64_t, int64_t>(n > 1 ? stride * es : 0, n);
   };
-  return {h.data, int64_t(head_dim) * es,
+  return {h.data, int64_t(head_dim) * es, heads_extent(h, B, L, head_dim, es),
           {axis(h.stride_b, B), axis(h.stride_row, L), axis(h.stride_head, h.n_heads)}};
 }
-Runs runs_of(const Arr &a) { return {a.p, a.bytes, {{0, 1}, {0, 1}, {0, 1}}}; }
 
 // True if no byte of `a` is one of `b`.  They meet where the distance between two
 // runs, b.p - a.p + sum t * step (t >= 0 for b's axes, <= 0 for a's), lies in
@@ -306,7 +306,6 @@ class Distance {
            reinterpret_cast<intptr_t>(a.p);
     for (const auto &[step, count] : b.ax) add(step, 0, count - 1);
     for (const auto &[step, count] : a.ax) add(step, 1 - count, 0);
-    std::sort(term_, term_ + n_, [](const Term &x, const Term &y) { return x.step > y.step; });
     for (int i = n_ - 1; i >= 0; --i) {
       term_[i].least = term_[i].lo * term_[i].step + (i + 1 < n_ ? term_[i + 1].least : 0);
       term_[i].most = term_[i].hi * term_[i].step + (i + 1 < n_ ? term_[i + 1].most : 0);
@@ -321,13 +320,15 @@ class Distance {
   };
   void add(int64_t step, int64_t lo, int64_t hi) {
     if (step == 0 || lo == hi) return;
-    for (int i = 0; i < n_; ++i) {
-      if (term_[i].step != step) continue;
+    int i = 0;  // the terms stand in falling order of their steps
+    while (i < n_ && term_[i].step > step) ++i;
+    if (i < n_ && term_[i].step == step) {
       term_[i].lo += lo;
       term_[i].hi += hi;
       return;
     }
-    term_[n_++] = Term{step, lo, hi, 0, 0};
+    for (int j = n_++; j > i; --j) term_[j] = term_[j - 1];
+    term_[i] = Term{step, lo, hi, 0, 0};
   }
   static __int128 floor_div(__int128 x, __int128 y) {  // y > 0
     return x / y - (x % y < 0 ? 1 : 0);
@@ -349,29 +350,35 @@ class Distance {
   Term term_[6];
   int n_ = 0, left_ = kMeetSteps;
 };
-bool runs_disjoint(const Runs &a, const Runs &b) { return !Distance(a, b).meets(); }
-
-// True if a and b lie in column blocks of rows of one pitch (q, k and v of a merged
-// projection), whatever their samples' steps: said without following those.
-bool column_blocks(const sol_heads &a, const sol_heads &b, int64_t B, int64_t L, int head_dim,
-                   int es) {
-  const int64_t ld = a.stride_row;
-  if (L == 1 || ld <= 0 || ld != b.stride_row) return false;
-  if (B > 1 && (a.stride_b % ld != 0 || b.stride_b % ld != 0)) return false;
-  const int64_t wa = ((a.n_heads - 1) * a.stride_head + head_dim) * es;
-  const int64_t wb = ((b.n_heads - 1) * b.stride_head + head_dim) * es;
-  int64_t c = (static_cast<int64_t>(reinterpret_cast<intptr_t>(b.data) -
-                                    reinterpret_cast<intptr_t>(a.data))) %
-              (ld * es);
-  if (c < 0) c += ld * es;
-  return wa <= c && c + wb <= ld * es;
+__attribute__((noinline)) bool runs_meet(const Runs &a, const Runs &b) {
+  return Distance(a, b).meets();
 }
 
-// True if the two share no byte.
-bool heads_disjoint(const sol_heads &a, const sol_heads &b, int64_t B, int64_t L, int head_dim,
-                    int es) {
-  return column_blocks(a, b, B, L, head_dim, es) ||
-         runs_disjoint(runs_of(a, B, L, head_dim, es), runs_of(b, B, L, head_dim, es));
+// True if a heads array and a contiguous one, or two heads arrays, share no byte.  Most
+// lie apart altogether.
+bool disjoint(const Runs &a, const Arr &b) {
+  return !spans_overlap(span_of(a.p, 1, 0, a.extent), span_of(b.p, 1, 0, b.bytes)) ||
+         !runs_meet(a, Runs{b.p, b.bytes, b.bytes, {{0, 1}, {0, 1}, {0, 1}}});
+}
+
+// True if a and b, heads arrays, lie in column blocks of rows of one pitch (q, k and v
+// of a merged projection), whatever their samples' steps: said without following those.
+bool column_blocks(const Runs &a, const Runs &b) {
+  const int64_t ld = a.ax[1].first;
+  if (ld <= 0 || ld != b.ax[1].first || a.ax[0].first % ld != 0 || b.ax[0].first % ld != 0)
+    return false;
+  const int64_t wa = (a.ax[2].second - 1) * a.ax[2].first + a.width;
+  const int64_t wb = (b.ax[2].second - 1) * b.ax[2].first + b.width;
+  int64_t c = (static_cast<int64_t>(reinterpret_cast<intptr_t>(b.p) -
+                                    reinterpret_cast<intptr_t>(a.p))) %
+              ld;
+  if (c < 0) c += ld;
+  return wa <= c && c + wb <= ld;
+}
+
+bool disjoint(const Runs &a, const Runs &b) {
+  return !spans_overlap(span_of(a.p, 1, 0, a.extent), span_of(b.p, 1, 0, b.extent)) ||
+         column_blocks(a, b) || !runs_meet(a, b);
 }
 
 HeadsArg heads_arg(const sol_heads *h, int es) {
@@ -450,24 +457,30 @@ sol_status rope_args(const char *fn, const sol_rope_plan *plan, const sol_positi
   const Arr small[] = {{"positions", pos->data, pos_bytes},
                        {"gamma_q", gamma_q, static_cast<int64_t>(hd) * es},
                        {"gamma_k", gamma_k, static_cast<int64_t>(hd) * es}};
+  Runs rx[2], rg[2], ro[2];
+  for (int t = 0; t < 2; ++t) {
+    if (x[t]) rx[t] = runs_of(*x[t], B, L, hd, es);
+    if (g[t]) rg[t] = runs_of(*g[t], B, L, hd, es);
+    if (out[t]) ro[t] = runs_of(*out[t], B, L, hd, es);
+  }
   for (int t = 0; t < 2; ++t) {
     if (!out[t]) continue;
-    const Runs ro = runs_of(*out[t], B, L, hd, es);
     for (const Arr &s : small)
-      if (s.p && !runs_disjoint(ro, runs_of(s)))
+      if (s.p && !disjoint(ro[t], s))
         return fail(SOL_ERR_INVALID_ARG, "%s: an output overlaps %s", fn, s.name);
     for (const Arr &o : other_outs)
-      if (o.p && o.bytes && !runs_disjoint(ro, runs_of(o)))
+      if (o.p && o.bytes && !disjoint(ro[t], o))
         return fail(SOL_ERR_INVALID_ARG, "%s: an output overlaps %s", fn, o.name);
     for (int u = 0; u < 2; ++u)
-      for (const sol_heads *h : {x[u], g[u]}) {
+      for (int in = 0; in < 2; ++in) {
+        const sol_heads *h = in ? g[u] : x[u];
         if (!h || (u == t && same_heads(*h, *out[t]))) continue;
-        if (!heads_disjoint(*out[t], *h, B, L, hd, es))
+        if (!disjoint(ro[t], in ? rg[u] : rx[u]))
           return fail(SOL_ERR_INVALID_ARG,
                       "%s: an output must equal its own input exactly or overlap no argument", fn);
       }
   }
-  if (out[1] && !heads_disjoint(*out[0], *out[1], B, L, hd, es))
+  if (out[1] && !disjoint(ro[0], ro[1]))
     return fail(SOL_ERR_INVALID_ARG, "%s: the two outputs overlap", fn);
   for (const Arr &o : other_outs) {
     if (!o.p || !o.bytes) continue;
@@ -479,9 +492,8 @@ sol_status rope_args(const char *fn, const sol_rope_plan *plan, const sol_positi
       if (&q != &o && q.p && q.bytes && spans_overlap(so, span_of(q.p, 1, 0, q.bytes)))
         return fail(SOL_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, o.name, q.name);
     for (int u = 0; u < 2; ++u)
-      for (const sol_heads *h : {x[u], g[u]})
-        if (h && !runs_disjoint(runs_of(o), runs_of(*h, B, L, hd, es)))
-          return fail(SOL_ERR_INVALID_ARG, "%s: %s overlaps an input", fn, o.name);
+      if ((x[u] && !disjoint(rx[u], o)) || (g[u] && !disjoint(rg[u], o)))
+        return fail(SOL_ERR_INVALID_ARG, "%s: %s overlaps an input", fn, o.name);
   }
 
   for (int t = 0; t < 2; ++t) {
